@@ -29,7 +29,7 @@
 extern "C" {
 #endif
 
-#define TRT_ABI_VERSION 13
+#define TRT_ABI_VERSION 14
 
 /* Status codes.  Every entry point returns one of these. */
 typedef enum {
@@ -489,6 +489,57 @@ trt_status trt_gemm_regtile(int64_t M, int64_t N, int64_t K,
 typedef enum { TRT_REDUCE_SUM = 0, TRT_REDUCE_MAX = 1, TRT_REDUCE_MIN = 2 } trt_reduce_op;
 trt_status trt_block_reduce(const void* x, int64_t n, int64_t block, int32_t dtype,
                             int32_t op, float* out, void* stream);
+
+/*
+ * The layer norm over the rows of a matrix, and its gradients.  No page
+ * defines it; it stands beside the block reduction above as the row reduction that
+ * a model puts in front of a product.  For each row x of cols elements, with
+ * mu = mean(x), v = mean((x - mu)^2) and h = (x - mu) / sqrt(v + eps):
+ *
+ *   trt_layernorm:      y = h * gamma + beta
+ *   trt_layernorm_bwd:  u = dy * gamma
+ *                       dx = (u - mean(u) - h * mean(u * h)) / sqrt(v + eps)
+ *                       dgamma = sum over the rows of dy * h
+ *                       dbeta  = sum over the rows of dy
+ *
+ * All sums are binary32 (two rounds over the row, the mean corrected in the
+ * second), each result is rounded once to its own type, and results repeat
+ * bit for bit.  The backward pass forms mu and v again from x, so the forward
+ * pass keeps nothing for it.
+ *
+ * x, y, dy, dx: rows of dtype (TRT_F16, TRT_BF16 or TRT_F32) with leading
+ * dimensions in elements: inputs >= 1, outputs >= cols.  gamma, beta, dgamma,
+ * dbeta: [cols] of param_dtype, which is dtype or TRT_F32.  gamma NULL stands
+ * for ones, beta NULL for zeros; dgamma and dbeta may each be NULL when that
+ * gradient is not wanted.  Any alignment to the element is allowed.  A row
+ * holds at most 65536 bytes (TRT_ERR_UNSUPPORTED beyond).  eps: finite and
+ * >= 0 (TRT_ERR_ARG).  No output may overlap any other buffer
+ * (TRT_ERR_OVERLAP): the norm does not run in place.  Elements between cols
+ * and the leading dimension are neither read nor written.
+ *
+ * workspace (backward pass with dgamma or dbeta; not touched otherwise):
+ * device memory of at least trt_layernorm_bwd_workspace_size(rows, cols,
+ * dtype) bytes, 16-byte aligned, contents unspecified before and after.  That
+ * size is a fixed number of partial sums of the parameter gradients; the
+ * function is host only and returns -1 on an argument error.  Calls that may
+ * overlap in time need a workspace each.
+ *
+ * Errors before any HIP call: TRT_ERR_SIZE (rows or cols outside [1, 2^30], an
+ * extent that overflows, a short workspace), TRT_ERR_STRIDE, TRT_ERR_NULL,
+ * TRT_ERR_ALIGN, TRT_ERR_OVERLAP, TRT_ERR_DTYPE, TRT_ERR_UNSUPPORTED,
+ * TRT_ERR_ARG; TRT_ERR_HIP if a launch fails.  Enqueued on `stream` (one kernel forward,
+ * one or two backward).
+ */
+trt_status trt_layernorm(int64_t rows, int64_t cols, const void* x, int64_t ldx,
+                         const void* gamma, const void* beta, float eps,
+                         void* y, int64_t ldy, int32_t dtype, int32_t param_dtype,
+                         void* stream);
+int64_t trt_layernorm_bwd_workspace_size(int64_t rows, int64_t cols, int32_t dtype);
+trt_status trt_layernorm_bwd(int64_t rows, int64_t cols, const void* dy, int64_t lddy,
+                             const void* x, int64_t ldx, const void* gamma, float eps,
+                             void* dx, int64_t lddx, void* dgamma, void* dbeta,
+                             int32_t dtype, int32_t param_dtype, void* workspace,
+                             int64_t workspace_bytes, void* stream);
 
 /*
  * trt_abi_version -- the ABI version of the loaded library (TRT_ABI_VERSION

@@ -9,6 +9,8 @@ call raises -- there is no fallback path.
     C = trt.gemm(A, B)                          # C = A @ B
     C = trt.gemm(A, B, bias=b, relu=True, residual=R)
     C = trt.gemm(At, B, opA="T")                # A stored transposed
+    y = trt.layernorm(x, gamma, beta)
+    dx, dgamma, dbeta = trt.layernorm_bwd(dy, x, gamma)
 """
 import ctypes
 import os
@@ -129,6 +131,14 @@ def lib():
         L.trt_gemm_regtile.restype = i32
         L.trt_choose_tile.argtypes = [i64, i64, i32, ctypes.POINTER(TileDesc)]
         L.trt_choose_tile.restype = i32
+        f32 = ctypes.c_float
+        L.trt_layernorm.argtypes = [i64, i64, vp, i64, vp, vp, f32, vp, i64, i32, i32, vp]
+        L.trt_layernorm.restype = i32
+        L.trt_layernorm_bwd_workspace_size.argtypes = [i64, i64, i32]
+        L.trt_layernorm_bwd_workspace_size.restype = i64
+        L.trt_layernorm_bwd.argtypes = [i64, i64, vp, i64, vp, i64, vp, f32, vp, i64, vp, vp, i32,
+                                        i32, vp, i64, vp]
+        L.trt_layernorm_bwd.restype = i32
         L.trt_abi_version.argtypes = []
         L.trt_abi_version.restype = i32
         L.trt_last_error.argtypes = []
@@ -551,3 +561,132 @@ def block_reduce(x, block, op=REDUCE_SUM, out=None):
         out = torch.empty(nb, dtype=torch.float32, device=x.device)
     block_reduce_raw(x.data_ptr(), n, block, _dtype_code(x), op, out.data_ptr(), _stream(x.device))
     return out
+
+
+# ---- the layer norm and its gradients ---------------------------------------------
+
+def _device(first, **others):
+    """The CUDA device that every tensor given lives on."""
+    dev = first.device
+    if dev.type != "cuda":
+        raise TrtError(ERR_ARG, "tensors must be on a GPU")
+    for name, t in others.items():
+        if t is not None and t.device != dev:
+            raise TrtError(ERR_ARG, f"{name} is on {t.device}, not on {dev}")
+    return dev
+
+
+def _on(dev, status_of):
+    """status_of(stream) with dev current (a launch goes to the current device)."""
+    torch = _torch()
+    stream = torch.cuda.current_stream(dev).cuda_stream or None
+    if torch.cuda.current_device() == dev.index:
+        return _check(status_of(stream))
+    with torch.cuda.device(dev):
+        _check(status_of(stream))
+
+
+def _rows(t, name):
+    """(rows, cols, leading dimension) of a tensor read as rows of its last
+    dimension, without a copy."""
+    if t.dim() == 0:
+        raise TrtError(ERR_ARG, f"{name} must have at least one dimension")
+    if t.dim() != 2:
+        try:
+            t = t.view(-1, t.size(-1))
+        except RuntimeError:
+            raise TrtError(ERR_STRIDE, f"{name} does not view as rows of its last dimension") from None
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise TrtError(ERR_STRIDE, f"{name} must have unit inner stride")
+    if rows > 1 and t.stride(0) < 1:
+        raise TrtError(ERR_STRIDE, f"{name}: rows must have a positive stride")
+    return rows, cols, t.stride(0) if rows > 1 else max(cols, 1)
+
+
+def _vector(t, name, n, dtype):
+    """Address of a contiguous vector of n elements of dtype, or None."""
+    if t is None:
+        return None
+    if t.dim() != 1 or t.numel() != n or (n > 1 and t.stride(0) != 1):
+        raise TrtError(ERR_SIZE, f"{name} must be contiguous with {n} elements")
+    if t.dtype != dtype:
+        raise TrtError(ERR_DTYPE, f"{name} must be {dtype}")
+    return t.data_ptr()
+
+
+def _like(out, t, name):
+    """out, or a new contiguous tensor of t's shape and dtype."""
+    torch = _torch()
+    if out is None:
+        return torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    if out.shape != t.shape or out.dtype != t.dtype:
+        raise TrtError(ERR_SIZE, f"{name} must be {list(t.shape)} of {t.dtype}")
+    return out
+
+
+def layernorm(x, gamma=None, beta=None, *, eps=1e-5, out=None):
+    """The layer norm of every row of x (its last dimension), times gamma plus
+    beta (ones and zeros where None): trt_layernorm.  x: float16, bfloat16 or
+    float32, rows of unit inner stride; gamma and beta: one dtype, x's or
+    float32.  out, if given, has x's shape and dtype and may not overlap the
+    inputs; otherwise a new tensor is returned.  Runs on torch's current
+    stream; no synchronisation.
+    """
+    rows, cols, ldx = _rows(x, "x")
+    param = next((t.dtype for t in (gamma, beta) if t is not None), x.dtype)
+    pdt = next((_dtype_code(t) for t in (gamma, beta) if t is not None), _dtype_code(x))
+    g, b = _vector(gamma, "gamma", cols, param), _vector(beta, "beta", cols, param)
+    out = _like(out, x, "out")
+    dev = _device(x, gamma=gamma, beta=beta, out=out)
+    _on(dev, lambda s: lib().trt_layernorm(rows, cols, x.data_ptr(), ldx, g, b, eps,
+                                           out.data_ptr(), _rows(out, "out")[2],
+                                           _dtype_code(x), pdt, s))
+    return out
+
+
+def layernorm_bwd_workspace_size(rows, cols, dtype=F16) -> int:
+    """trt_layernorm_bwd_workspace_size: bytes of workspace of the backward pass."""
+    n = lib().trt_layernorm_bwd_workspace_size(rows, cols, dtype)
+    if n < 0:
+        raise TrtError(ERR_ARG, last_error())
+    return n
+
+
+def layernorm_bwd(dy, x, gamma=None, *, eps=1e-5, params=True, dx=None, dgamma=None, dbeta=None,
+                  workspace=None):
+    """The gradients of layernorm at x for dy: (dx, dgamma, dbeta), by
+    trt_layernorm_bwd.  dy has x's shape and dtype; eps is the forward pass's.
+    dgamma and dbeta have gamma's dtype (float32 without a gamma, unless the
+    dgamma or dbeta given says otherwise); with params=False neither is
+    computed and both are None.  dx, dgamma, dbeta and workspace (a uint8
+    tensor of layernorm_bwd_workspace_size(...) bytes) are written if given,
+    else allocated.  Runs on torch's current stream; no synchronisation.
+    """
+    torch = _torch()
+    rows, cols, ldx = _rows(x, "x")
+    if dy.shape != x.shape or dy.dtype != x.dtype:
+        raise TrtError(ERR_SIZE, f"dy must be {list(x.shape)} of {x.dtype}")
+    param = next((t for t in (gamma, dgamma, dbeta) if t is not None), None)
+    pdtype = torch.float32 if param is None else param.dtype
+    pdt = F32 if param is None else _dtype_code(param)
+    dx = _like(dx, x, "dx")
+    if params:
+        need = layernorm_bwd_workspace_size(rows, cols, _dtype_code(x))
+        if dgamma is None:
+            dgamma = torch.empty(cols, dtype=pdtype, device=x.device)
+        if dbeta is None:
+            dbeta = torch.empty(cols, dtype=pdtype, device=x.device)
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    else:
+        dgamma = dbeta = workspace = None
+    g, dg, db = (_vector(t, name, cols, pdtype) for t, name in
+                 ((gamma, "gamma"), (dgamma, "dgamma"), (dbeta, "dbeta")))
+    dev = _device(x, dy=dy, gamma=gamma, dx=dx, dgamma=dgamma, dbeta=dbeta, workspace=workspace)
+    ws, wsb = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    _on(dev, lambda s: lib().trt_layernorm_bwd(rows, cols, dy.data_ptr(), _rows(dy, "dy")[2],
+                                               x.data_ptr(), ldx, g, eps, dx.data_ptr(),
+                                               _rows(dx, "dx")[2], dg, db, _dtype_code(x), pdt,
+                                               ws or None, wsb, s))
+    return dx, dgamma, dbeta

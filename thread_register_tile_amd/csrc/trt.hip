@@ -13,26 +13,15 @@
 #include "launch.hpp"
 #include "reduce.hpp"
 #include "regtile.hpp"
+#include "status.hpp"
 #include "tiles.hpp"
 #include "validate.hpp"
 
 namespace {
 
-thread_local std::string g_err;
-
-trt_status fail(trt_status s, const std::string& msg) {
-  g_err = msg;
-  return s;
-}
-
-// The status of one launch, as the runtime returned it for that launch.
-trt_status launched(hipError_t e, const char* what) {
-  if (e != hipSuccess)
-    return fail(TRT_ERR_HIP, std::string(what) + ": " + hipGetErrorString(e));
-  g_err.clear();
-  return TRT_OK;
-}
-
+using trt::fail;
+using trt::g_err;
+using trt::launched;
 using trt::GemmArgs;
 
 // ---- compiled tiles ------------------------------------------------------------
