@@ -542,6 +542,77 @@ trt_status trt_layernorm_bwd(int64_t rows, int64_t cols, const void* dy, int64_t
                              int64_t workspace_bytes, void* stream);
 
 /*
+ * The softmax cross entropy of a linear vocabulary head, without its logits,
+ * and its gradients.  No page defines it; it is the library's product with
+ * another epilogue.  With z = X . W^T (x: [tokens, width], w: [vocab, width],
+ * the logits [tokens, vocab] are never stored):
+ *
+ *   trt_linear_xent:      lse[t]  = log sum_v exp z[t,v]
+ *                         loss[t] = lse[t] - z[t, target[t]]
+ *   trt_linear_xent_bwd:  g[t,v] = exp(z[t,v] - lse[t]) * (dloss[t] + dlse[t])
+ *                                  - (v == target[t]) * dloss[t]
+ *                         dx = g . W,   dw = g^T . X
+ *
+ * No reduction over the tokens is applied: a mean is dloss[t] = 1 / count.
+ * dlse (NULL: none) is the gradient of whatever else depends on lse, such as
+ * a penalty on its square.
+ *
+ * Tokens whose target equals ignore_index take part in nothing: loss = lse =
+ * 0, a zero row in dx, no share of dw, whatever their row of x holds; they
+ * cost next to no time either.  So do, in the backward pass, tokens
+ * whose dloss and dlse are both zero.  A target outside [0, vocab) that
+ * is not ignore_index gives loss = NaN (lse is the true one) and, in the
+ * backward pass, a row of NaN in dx and NaN in dw: it is not read out of range.
+ * A NaN or infinity among a live token's logits makes its loss NaN.
+ *
+ * x, w: dtype (in_dtype) TRT_F16 or TRT_BF16, ldx, ldw >= width; target:
+ * [tokens] int64; loss, lse: [tokens] binary32.  dx: [tokens, width], dw:
+ * [vocab, width] of out_dtype (TRT_F16, TRT_BF16 or TRT_F32), lddx, lddw >=
+ * width; either may be NULL, not both.  dloss[t * inc_dloss], dlse[t *
+ * inc_dlse]: binary32, increments >= 0 (0: one value for all tokens).  lse is
+ * the forward pass's.  Logits, statistics and all sums are binary32.  The
+ * backward pass works through the vocabulary in pieces of `piece` entries
+ * (0: the library's choice; else a multiple of 64 up to 2^20, TRT_ERR_ARG
+ * otherwise) and rounds g, with the tokens' weights max(|dloss|, |dloss +
+ * dlse|) taken out, once to in_dtype; with weights that differ between
+ * tokens it rounds X times their ratio to the largest as well.  In binary16
+ * that loses bits for tokens whose weight is below 2^-14 of the largest.
+ * Results repeat bit for bit.
+ *
+ * workspace: device memory of at least trt_linear_xent_workspace_size(tokens,
+ * vocab, width) or trt_linear_xent_bwd_workspace_size(tokens, vocab, width,
+ * piece) bytes, 16-byte aligned, contents unspecified before and after; the
+ * backward pass's holds one piece of g and dx's sums.  Calls that may overlap
+ * in time need a workspace each.  The size functions are host only and return
+ * -1 on an argument error.
+ *
+ * Any strides and alignments to the element are allowed; 16-byte aligned x
+ * and w with width, ldx and ldw multiples of 8 take the fast kernels.  No
+ * output and no workspace may overlap any other buffer (TRT_ERR_OVERLAP).
+ * 1 <= tokens <= 2^23, 1 <= vocab <= 2^30, 1 <= width <= 2^20, and any two of
+ * them give fewer than 2^24 tiles of 128x128 (TRT_ERR_SIZE).  Errors before any HIP call: TRT_ERR_SIZE,
+ * TRT_ERR_STRIDE, TRT_ERR_NULL, TRT_ERR_ALIGN, TRT_ERR_OVERLAP,
+ * TRT_ERR_DTYPE, TRT_ERR_ARG; TRT_ERR_HIP if a launch fails.  Enqueued on
+ * `stream`: two or three kernels forward; backward three, and up to three for each piece.
+ */
+int64_t trt_linear_xent_workspace_size(int64_t tokens, int64_t vocab, int64_t width);
+trt_status trt_linear_xent(int64_t tokens, int64_t vocab, int64_t width,
+                           const void* x, int64_t ldx, const void* w, int64_t ldw,
+                           const int64_t* target, int64_t ignore_index,
+                           float* loss, float* lse, int32_t dtype,
+                           void* workspace, int64_t workspace_bytes, void* stream);
+int64_t trt_linear_xent_bwd_workspace_size(int64_t tokens, int64_t vocab, int64_t width,
+                                           int64_t piece);
+trt_status trt_linear_xent_bwd(int64_t tokens, int64_t vocab, int64_t width,
+                               const void* x, int64_t ldx, const void* w, int64_t ldw,
+                               const int64_t* target, int64_t ignore_index,
+                               const float* lse, const float* dloss, int64_t inc_dloss,
+                               const float* dlse, int64_t inc_dlse,
+                               void* dx, int64_t lddx, void* dw, int64_t lddw,
+                               int32_t in_dtype, int32_t out_dtype, int64_t piece,
+                               void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
  * trt_abi_version -- the ABI version of the loaded library (TRT_ABI_VERSION
  * at build time).  "Named layouts", section "Runtime and compilation": the
  * launch ABI keeps versioned layout obligations so that caching and reload

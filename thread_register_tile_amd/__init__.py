@@ -11,6 +11,8 @@ call raises -- there is no fallback path.
     C = trt.gemm(At, B, opA="T")                # A stored transposed
     y = trt.layernorm(x, gamma, beta)
     dx, dgamma, dbeta = trt.layernorm_bwd(dy, x, gamma)
+    loss, lse = trt.linear_xent(x, W, target)   # cross entropy of x @ W.T
+    dx, dW = trt.linear_xent_bwd(x, W, target, lse, dloss)
 """
 import ctypes
 import os
@@ -139,6 +141,16 @@ def lib():
         L.trt_layernorm_bwd.argtypes = [i64, i64, vp, i64, vp, i64, vp, f32, vp, i64, vp, vp, i32,
                                         i32, vp, i64, vp]
         L.trt_layernorm_bwd.restype = i32
+        L.trt_linear_xent_workspace_size.argtypes = [i64, i64, i64]
+        L.trt_linear_xent_workspace_size.restype = i64
+        L.trt_linear_xent.argtypes = [i64, i64, i64, vp, i64, vp, i64, vp, i64, vp, vp, i32, vp, i64,
+                                      vp]
+        L.trt_linear_xent.restype = i32
+        L.trt_linear_xent_bwd_workspace_size.argtypes = [i64, i64, i64, i64]
+        L.trt_linear_xent_bwd_workspace_size.restype = i64
+        L.trt_linear_xent_bwd.argtypes = [i64, i64, i64, vp, i64, vp, i64, vp, i64, vp, vp, i64, vp,
+                                          i64, vp, i64, vp, i64, i32, i32, i64, vp, i64, vp]
+        L.trt_linear_xent_bwd.restype = i32
         L.trt_abi_version.argtypes = []
         L.trt_abi_version.restype = i32
         L.trt_last_error.argtypes = []
@@ -690,3 +702,134 @@ def layernorm_bwd(dy, x, gamma=None, *, eps=1e-5, params=True, dx=None, dgamma=N
                                                _rows(dx, "dx")[2], dg, db, _dtype_code(x), pdt,
                                                ws or None, wsb, s))
     return dx, dgamma, dbeta
+
+
+# ---- the linear cross entropy and its gradients -------------------------------------
+
+def _xent_inputs(x, w, target):
+    """(tokens, vocab, width, ldx, ldw) of a head's input, weight and targets."""
+    torch = _torch()
+    tokens, width, ldx = _rows(x, "x")
+    if w.dim() != 2 or w.size(1) != width:
+        raise TrtError(ERR_SIZE, f"w must be [vocab, {width}]")
+    vocab, _, ldw = _rows(w, "w")
+    if w.dtype != x.dtype:
+        raise TrtError(ERR_DTYPE, "x and w dtypes differ")
+    if target.dtype != torch.int64:
+        raise TrtError(ERR_DTYPE, "target must be int64")
+    if target.shape != x.shape[:-1] or not target.is_contiguous():
+        raise TrtError(ERR_SIZE, f"target must be contiguous of shape {list(x.shape[:-1])}")
+    return tokens, vocab, width, ldx, ldw
+
+
+def _per_token(t, name, shape):
+    """(address, increment) of a float32 value for each token; a tensor of one
+    element, or one expanded from it, stands for all tokens."""
+    torch = _torch()
+    if t is None:
+        return None, 0
+    if t.dtype != torch.float32:
+        raise TrtError(ERR_DTYPE, f"{name} must be float32")
+    if t.numel() == 1:
+        return t.data_ptr(), 0
+    if t.shape != shape:
+        raise TrtError(ERR_SIZE, f"{name} must have shape {list(shape)} or one element")
+    if all(st == 0 for st, n in zip(t.stride(), t.shape) if n > 1):
+        return t.data_ptr(), 0
+    if t.dim() == 1:
+        return t.data_ptr(), t.stride(0)
+    if not t.is_contiguous():
+        raise TrtError(ERR_STRIDE, f"{name} must be contiguous or one-dimensional")
+    return t.data_ptr(), 1
+
+
+def _tokens_out(t, name, like):
+    """t, or a new float32 tensor of like's shape."""
+    torch = _torch()
+    if t is None:
+        return torch.empty(like.shape, dtype=torch.float32, device=like.device)
+    if t.shape != like.shape or t.dtype != torch.float32 or not t.is_contiguous():
+        raise TrtError(ERR_SIZE, f"{name} must be contiguous float32 of shape {list(like.shape)}")
+    return t
+
+
+def _workspace(ws, need, device):
+    return _torch().empty(need, dtype=_torch().uint8, device=device) if ws is None else ws
+
+
+def linear_xent_workspace_size(tokens, vocab, width) -> int:
+    """trt_linear_xent_workspace_size: bytes of workspace of the forward pass."""
+    n = lib().trt_linear_xent_workspace_size(tokens, vocab, width)
+    if n < 0:
+        raise TrtError(ERR_ARG, last_error())
+    return n
+
+
+def linear_xent(x, w, target, *, ignore_index=-100, loss=None, lse=None, workspace=None):
+    """The softmax cross entropy of the logits x @ w.T, which are not stored:
+    (loss, lse) per token, float32, by trt_linear_xent.  x: [..., width] and w:
+    [vocab, width], float16 or bfloat16; target: int64 of x's leading shape.
+    Tokens whose target is ignore_index have loss and lse 0.  loss, lse and
+    workspace (a uint8 tensor of linear_xent_workspace_size(...) bytes) are
+    written if given, else allocated.  Runs on torch's current stream; no
+    synchronisation.
+    """
+    tokens, vocab, width, ldx, ldw = _xent_inputs(x, w, target)
+    workspace = _workspace(workspace, linear_xent_workspace_size(tokens, vocab, width), x.device)
+    loss, lse = _tokens_out(loss, "loss", target), _tokens_out(lse, "lse", target)
+    dev = _device(x, w=w, target=target, loss=loss, lse=lse, workspace=workspace)
+    _on(dev, lambda s: lib().trt_linear_xent(tokens, vocab, width, x.data_ptr(), ldx, w.data_ptr(), ldw,
+                                             target.data_ptr(), ignore_index, loss.data_ptr(),
+                                             lse.data_ptr(), _dtype_code(x), workspace.data_ptr(),
+                                             workspace.numel() * workspace.element_size(), s))
+    return loss, lse
+
+
+def linear_xent_bwd_workspace_size(tokens, vocab, width, piece=0) -> int:
+    """trt_linear_xent_bwd_workspace_size: bytes of workspace of the backward pass."""
+    n = lib().trt_linear_xent_bwd_workspace_size(tokens, vocab, width, piece)
+    if n < 0:
+        raise TrtError(ERR_ARG, last_error())
+    return n
+
+
+def linear_xent_bwd(x, w, target, lse, dloss, dlse=None, *, ignore_index=-100, need_dx=True,
+                    need_dw=True, out_dtype=None, piece=0, dx=None, dw=None, workspace=None):
+    """The gradients (dx, dw) of linear_xent for the upstream gradients dloss
+    and dlse (None: zero), by trt_linear_xent_bwd.  x, w, target and lse are the
+    forward pass's; dloss and dlse: float32 per token, or one element for all.
+    dx and dw have out_dtype (default: x's dtype, or the dtype of the one
+    given); the one not needed is None.  piece: vocabulary entries at a time
+    (0: the library's choice).  dx, dw and workspace (a uint8 tensor of
+    linear_xent_bwd_workspace_size(...) bytes) are written if given, else
+    allocated.  Runs on torch's current stream; no synchronisation.
+    """
+    torch = _torch()
+    tokens, vocab, width, ldx, ldw = _xent_inputs(x, w, target)
+    if lse.shape != target.shape or lse.dtype != torch.float32 or not lse.is_contiguous():
+        raise TrtError(ERR_SIZE, f"lse must be contiguous float32 of shape {list(target.shape)}")
+    (dl, dl_inc), (de, de_inc) = _per_token(dloss, "dloss", target.shape), _per_token(dlse, "dlse", target.shape)
+    if dl is None:
+        raise TrtError(ERR_NULL, "dloss must be given")
+    given = next((t.dtype for t in (dx, dw) if t is not None), x.dtype)
+    odt = out_dtype or given
+
+    def output(t, like, need, name):
+        if not need:
+            return None, 0
+        if t is None:
+            t = torch.empty(like.shape, dtype=odt, device=like.device)
+        elif t.shape != like.shape or t.dtype != odt:
+            raise TrtError(ERR_SIZE, f"{name} must be {list(like.shape)} of {odt}")
+        return t, _rows(t, name)[2]
+
+    (dx, lddx), (dw, lddw) = output(dx, x, need_dx, "dx"), output(dw, w, need_dw, "dw")
+    out = next((t for t in (dx, dw) if t is not None), x)
+    workspace = _workspace(workspace, linear_xent_bwd_workspace_size(tokens, vocab, width, piece), x.device)
+    dev = _device(x, w=w, target=target, lse=lse, dloss=dloss, dlse=dlse, dx=dx, dw=dw, workspace=workspace)
+    _on(dev, lambda s: lib().trt_linear_xent_bwd(
+        tokens, vocab, width, x.data_ptr(), ldx, w.data_ptr(), ldw, target.data_ptr(), ignore_index,
+        lse.data_ptr(), dl, dl_inc, de, de_inc, None if dx is None else dx.data_ptr(), lddx,
+        None if dw is None else dw.data_ptr(), lddw, _dtype_code(x), _dtype_code(out), piece,
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), s))
+    return dx, dw

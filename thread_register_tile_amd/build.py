@@ -15,7 +15,9 @@ SOURCES = ["trt.hip", "kern_tiny.hip", "kern_64.hip", "kern_128.hip", "kern_256.
            "kern_256f.hip", "kern_dma256_f16_ak.hip", "kern_dma256_f16_am.hip",
            "kern_dma256_bf16_ak.hip", "kern_dma256_bf16_am.hip", "kern_dma192_f16.hip",
            "kern_dma192_bf16.hip", "kern_dma128.hip", "kern_skinny.hip", "kern_reduce.hip", "kern_f32.hip",
-           "kern_regtile.hip", "trt_norm.hip", "kern_layernorm.hip"]
+           "kern_regtile.hip", "trt_norm.hip", "kern_layernorm.hip", "trt_xent.hip",
+           "kern_xent.hip", "kern_xent_stats.hip", "kern_xent_grad.hip", "kern_xent_input.hip",
+           "kern_xent_weight.hip"]
 # Per-file flags.  The binary32 kernels keep their accumulators in ordinary
 # VGPRs: left to itself the compiler puts them in AGPRs and moves half of
 # them through VGPRs every K step.

@@ -168,8 +168,11 @@ struct DmaOperand {
   uint32_t tail_drop;    // k-contiguous: 2^31 where the lane's chunk lies past K
                          // on the last, partial K step, else 0
 
+  // rows(r): the stored row of tile-space row r (k-contiguous operands), or a
+  // negative number where there is none: it reads as zero.
+  template <class Rows>
   __device__ __forceinline__ void init(const uint16_t* X, int64_t ld, int64_t ext, int row0,
-                                       int wave, int lane, int K) {
+                                       int wave, int lane, int K, Rows rows) {
     cur = reinterpret_cast<const char*>(X) - BIAS;
     rem = (uint32_t)ext + BIAS;
     int kchunk = 0;
@@ -179,8 +182,11 @@ struct DmaOperand {
       uint32_t off;
       if (KC) {
         const int r = TL::template kc_slot_row<R>(s), g = TL::template kc_slot_g<R>(s);
-        off = (uint32_t)(((int64_t)(row0 + r) * ld + 8 * g) * 2);
+        const auto row = rows(row0 + r);
+        off = (uint32_t)(((int64_t)row * ld + 8 * g) * 2);
         kchunk = 8 * g;
+        if constexpr (!std::is_same_v<Rows, SameRows>)
+          if (row < 0) off = 0x80000000u;   // beyond every record count
       } else {
         const int k = TL::template mn_slot_k<R>(s), c = TL::template mn_slot_c<R>(s);
         off = (uint32_t)(((int64_t)k * ld + row0 + 8 * c) * 2);
@@ -611,6 +617,24 @@ struct FragReader {
   }
 };
 
+// What a kernel does around the product: the GEMM's own epilogue here, the
+// cross entropy's in xent.hpp.  Args extends GemmArgs; begin(p) may narrow the
+// problem from device memory or the grid's second axis (false: the workgroup
+// has no tile); rows(p) maps A's rows to stored ones; finish() takes the
+// tile's accumulators, with every LDS stage free for its use.
+struct GemmEpilogue {
+  using Args = GemmArgs;
+  __device__ static bool begin(Args&) { return true; }
+  __device__ static SameRows rows(const Args&) { return {}; }
+  template <class TL, int DT>
+  __device__ __forceinline__ static void finish(const Args& p, f32x4 (&acc)[TL::FM][TL::FN],
+                                                char* lds, int m0, int n0, int t) {
+    with_out_type(p.out_dt, [&]<int OT>() {
+      epilogue_lds<TL, OT>(p, acc, reinterpret_cast<float*>(lds), m0, n0, t);
+    });
+  }
+};
+
 // Per K step one block of FM*FN products on one set of operand registers:
 // the first half (fragment rows 0..FM/2-1 against every column, column by
 // column) with this thread's copies of step kt+3 and the reads of the step's
@@ -619,8 +643,8 @@ struct FragReader {
 // FM/2..FM-1, column by column) with the next stage's rows 0..FM/2-1 and
 // columns read into the registers as they die (each column right after its
 // last product).
-template <class TL, int DT, bool A_KC, bool B_KC, int NS = 4>
-__global__ __launch_bounds__(TL::THREADS, 1) void gemm_dma_kernel(GemmArgs p) {
+template <class TL, int DT, bool A_KC, bool B_KC, int NS = 4, class EPI = GemmEpilogue>
+__global__ __launch_bounds__(TL::THREADS, 1) void gemm_dma_kernel(typename EPI::Args p) {
   static_assert(TL::BK == 32 && TL::MF == 16, "32-wide K steps of 16x16x32 fragments");
   static_assert(NS >= 3, "copies at least two steps ahead");
   constexpr int BM = TL::BM, BN = TL::BN, FM = TL::FM, FN = TL::FN;
@@ -637,14 +661,15 @@ __global__ __launch_bounds__(TL::THREADS, 1) void gemm_dma_kernel(GemmArgs p) {
 
   const int t = threadIdx.x;
   const int lane = t & 63, wave = t >> 6;
+  if (!EPI::begin(p)) return;
   int tm, tn;
   tile_of<8>(blockIdx.x, p.tiles_m, p.tiles_n, tm, tn);
   const int m0 = tm * BM, n0 = tn * BN;
 
   OpA a;
   OpB b;
-  a.init(p.A, p.lda, p.a_bytes, m0, wave, lane, p.K);
-  b.init(p.B, p.ldb, p.b_bytes, n0, wave, lane, p.K);
+  a.init(p.A, p.lda, p.a_bytes, m0, wave, lane, p.K, EPI::rows(p));
+  b.init(p.B, p.ldb, p.b_bytes, n0, wave, lane, p.K, SameRows{});
 
   const int nk = (p.K + 31) / 32;
   // LDS address of this wave's first copy slot in each operand region of
@@ -773,9 +798,7 @@ __global__ __launch_bounds__(TL::THREADS, 1) void gemm_dma_kernel(GemmArgs p) {
   __builtin_amdgcn_s_waitcnt(waitcnt_lgkm(0));
   __syncthreads();
 
-  with_out_type(p.out_dt, [&]<int OT>() {
-    epilogue_lds<TL, OT>(p, acc, reinterpret_cast<float*>(lds_raw), m0, n0, t);
-  });
+  EPI::template finish<TL, DT>(p, acc, lds_raw, m0, n0, t);
 }
 
 }  // namespace trt

@@ -236,6 +236,11 @@ __device__ __forceinline__ void tile_of(int bid, int tiles_m, int tiles_n, int& 
   tn = in / rows;
 }
 
+// A's rows as they are stored: row r of the problem is row r of the array.
+struct SameRows {
+  __device__ int operator()(int r) const { return r; }
+};
+
 // ---- global -> registers ---------------------------------------------------------
 
 // 8 consecutive 16-bit elements starting at src, n of them valid (the rest
@@ -250,21 +255,29 @@ __device__ __forceinline__ u32x4 load8(const uint16_t* src, int n) {
                h[6] | (h[7] << 16)};
 }
 
-// Operand stored with k contiguous: element (r, k) at X[(row0 + r)*ld + k].
+// Operand stored with k contiguous: element (r, k) at X[rows(row0 + r)*ld + k],
+// zero where rows() is negative.
 template <class TL, int R, bool VEC>
 struct KContigOperand {
   using Map = typename TL::template KContig<R>;
   static constexpr int ITERS = Map::ITERS;
   u32x4 st[ITERS];
 
-  template <bool CHECK>
+  template <bool CHECK, class Rows = SameRows>
   __device__ __forceinline__ void load(const uint16_t* X, int64_t ld, int row0, int rows,
-                                       int k0, int K, int t) {
+                                       int k0, int K, int t, Rows stored = {}) {
 #pragma unroll
     for (int i = 0; i < ITERS; ++i) {
       if (Map::ITEMS % TL::THREADS != 0 && !Map::active(t, i)) continue;
       const int r = row0 + Map::row(t, i);
       const int k = k0 + 8 * Map::g(t, i);
+      if constexpr (!std::is_same_v<Rows, SameRows>) {
+        int n = K - k;
+        n = n < 0 ? 0 : (n > 8 ? 8 : n);
+        const int from = r < rows ? stored(r) : -1;
+        st[i] = load8<VEC>(X + (int64_t)(from < 0 ? 0 : from) * ld + k, from < 0 ? 0 : n);
+        continue;
+      }
       const uint16_t* src = X + (int64_t)r * ld + k;
       if (!CHECK) {
         st[i] = load8<VEC>(src, 8);
@@ -460,19 +473,33 @@ __device__ __forceinline__ void epilogue_store(const GemmArgs& p,
   }
 }
 
+// What the kernel does around the product; the pipelined kernel's counterpart
+// (gemm_dma.hpp) explains the members.
+struct GenericEpilogue {
+  using Args = GemmArgs;
+  __device__ static bool begin(Args&) { return true; }
+  __device__ static SameRows rows(const Args&) { return {}; }
+  template <class TL, int DT>
+  __device__ __forceinline__ static void finish(const Args& p, f32x4 (&acc)[TL::FM][TL::FN],
+                                                char*, int m0, int n0, int t) {
+    epilogue_store<TL>(p, acc, m0, n0, t & 63, t >> 6);
+  }
+};
+
 // ---- the kernel -------------------------------------------------------------------
 
 // A_KC: A stored with k contiguous (op N); otherwise A^T (op T).
 // B_KC: B stored with k contiguous (B^T, op T); otherwise row-major (op N).
 // VEC:  16-byte aligned operand rows, so chunks load as one vector.
-template <class TL, int DT, bool A_KC, bool B_KC, bool VEC>
-__global__ __launch_bounds__(TL::THREADS) void gemm_kernel(GemmArgs p) {
+template <class TL, int DT, bool A_KC, bool B_KC, bool VEC, class EPI = GenericEpilogue>
+__global__ __launch_bounds__(TL::THREADS) void gemm_kernel(typename EPI::Args p) {
   static_assert(TL::MF == 16, "the generic kernel runs 16x16x32 fragments");
   constexpr int G = TL::G;
   __shared__ u32x4 lds[2][(TL::BM + TL::BN) * G];
 
   const int t = threadIdx.x;
   const int lane = t & 63, wave = t >> 6;
+  if (!EPI::begin(p)) return;
   int tm, tn;
   tile_of<8>(blockIdx.x, p.tiles_m, p.tiles_n, tm, tn);
   const int m0 = tm * TL::BM, n0 = tn * TL::BN;
@@ -489,13 +516,17 @@ __global__ __launch_bounds__(TL::THREADS) void gemm_kernel(GemmArgs p) {
 
   const int nk = (p.K + TL::BK - 1) / TL::BK;
 
+  auto load_a = [&]<bool CHECK>(int k0) {
+    if constexpr (A_KC) a.template load<CHECK>(p.A, p.lda, m0, p.M, k0, p.K, t, EPI::rows(p));
+    else a.template load<CHECK>(p.A, p.lda, m0, p.M, k0, p.K, t);
+  };
   auto load_step = [&](int kt) {
     const int k0 = kt * TL::BK;
     if (full_mn && k0 + TL::BK <= p.K) {
-      a.template load<false>(p.A, p.lda, m0, p.M, k0, p.K, t);
+      load_a.template operator()<false>(k0);
       b.template load<false>(p.B, p.ldb, n0, p.N, k0, p.K, t);
     } else {
-      a.template load<true>(p.A, p.lda, m0, p.M, k0, p.K, t);
+      load_a.template operator()<true>(k0);
       b.template load<true>(p.B, p.ldb, n0, p.N, k0, p.K, t);
     }
   };
@@ -536,7 +567,7 @@ __global__ __launch_bounds__(TL::THREADS) void gemm_kernel(GemmArgs p) {
     __syncthreads();
   }
 
-  epilogue_store<TL>(p, acc, m0, n0, lane, wave);
+  EPI::template finish<TL, DT>(p, acc, reinterpret_cast<char*>(lds), m0, n0, t);
 }
 
 }  // namespace trt

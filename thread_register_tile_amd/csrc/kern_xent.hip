@@ -1,0 +1,36 @@
+// kern_xent.hip -- the cross entropy's small kernels.
+#include "launch.hpp"
+#include "xent_rows.hpp"
+
+namespace trt {
+
+hipError_t launch_xent_prep(const XentPrepArgs& a, hipStream_t s) {
+  return launch(xent_prep_kernel, dim3(1), dim3(kPrepThreads), 0, s, a);
+}
+
+// Rows to a workgroup: 64, so that a wave reads whole lines of a tile's
+// pairs; fewer tokens take fewer, so that more threads share a row's tiles.
+hipError_t launch_xent_combine(const XentCombineArgs& a, hipStream_t s) {
+  auto run = [&]<int R>() {
+    return launch(xent_combine_kernel<R>, dim3((a.tokens + R - 1) / R), dim3(256), 0, s, a);
+  };
+  if (a.tokens <= 4) return run.template operator()<1>();
+  if (a.tokens <= 256) return run.template operator()<8>();
+  return run.template operator()<64>();
+}
+
+hipError_t launch_xent_rows(const XentRowsArgs& a, int dt, hipStream_t s) {
+  const dim3 grid(a.prep.tokens), block(256);
+  if (dt == DT_F16) return launch(xent_rows_kernel<DT_F16>, grid, block, 0, s, a);
+  return launch(xent_rows_kernel<DT_BF16>, grid, block, 0, s, a);
+}
+
+hipError_t launch_xent_input_finish(const XentInputFinishArgs& a, int64_t tokens, int odt,
+                                    hipStream_t s) {
+  const dim3 grid((unsigned)tokens), block(256);
+  if (odt == DT_F16) return launch(xent_input_finish_kernel<DT_F16>, grid, block, 0, s, a);
+  if (odt == DT_BF16) return launch(xent_input_finish_kernel<DT_BF16>, grid, block, 0, s, a);
+  return launch(xent_input_finish_kernel<DT_F32>, grid, block, 0, s, a);
+}
+
+}  // namespace trt

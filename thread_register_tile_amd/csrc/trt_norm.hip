@@ -2,28 +2,14 @@
 // Declarations and contracts are in include/trt.h.
 #include <cmath>
 
+#include "buffers.hpp"
 #include "norm.hpp"
-#include "status.hpp"
-#include "validate.hpp"
 
 namespace {
 
-using trt::Extent;
+using trt::Buf;
+using trt::check_buffers;
 using trt::fail;
-
-// A caller's buffer: a rows x cols matrix with leading dimension ld, named
-// for the messages.  A null base is an absent optional buffer.
-struct Buf {
-  const char* name;
-  const void* base;
-  int64_t rows, cols, ld, esize;
-  Extent extent() const {
-    int64_t bytes = 0;
-    if (base) trt::span_bytes(rows, cols, ld, bytes, esize);
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(base);
-    return Extent{lo, lo + (uintptr_t)bytes};
-  }
-};
 
 trt_status check_sizes(int64_t rows, int64_t cols, float eps, int32_t dtype, int32_t param_dtype) {
   if (rows < 1 || cols < 1 || rows > trt::kMaxDim || cols > trt::kMaxDim)
@@ -35,29 +21,6 @@ trt_status check_sizes(int64_t rows, int64_t cols, float eps, int32_t dtype, int
   if (!(eps >= 0.f) || std::isinf(eps)) return fail(TRT_ERR_ARG, "eps must be finite and not negative");
   if (cols * trt::elem_bytes(dtype) > trt::kNormMaxRowBytes)
     return fail(TRT_ERR_UNSUPPORTED, "a row must not exceed 65536 bytes");
-  return TRT_OK;
-}
-
-// Every buffer's alignment, stride and extent, then each written buffer
-// against every other one.  The first n_out buffers are written.
-template <size_t N>
-trt_status check_buffers(const Buf (&b)[N], size_t n_out) {
-  for (size_t i = 0; i < N; ++i) {
-    if (!b[i].base) continue;
-    if (i < n_out ? b[i].ld < b[i].cols : b[i].ld < 1)
-      return fail(TRT_ERR_STRIDE, std::string(b[i].name) +
-                                      (i < n_out ? ": rows written must not overlap (ld >= cols)"
-                                                 : ": leading dimension must be >= 1"));
-    if (reinterpret_cast<uintptr_t>(b[i].base) & (uintptr_t)(b[i].esize - 1))
-      return fail(TRT_ERR_ALIGN, std::string(b[i].name) + " must be aligned to its element");
-    int64_t bytes;
-    if (!trt::span_bytes(b[i].rows, b[i].cols, b[i].ld, bytes, b[i].esize))
-      return fail(TRT_ERR_SIZE, std::string(b[i].name) + ": extent overflows");
-  }
-  for (size_t i = 0; i < n_out; ++i)
-    for (size_t j = 0; j < N; ++j)
-      if (i != j && trt::overlaps(b[i].extent(), b[j].extent()))
-        return fail(TRT_ERR_OVERLAP, std::string(b[i].name) + " overlaps " + b[j].name);
   return TRT_OK;
 }
 
@@ -110,13 +73,7 @@ trt_status trt_layernorm_bwd(int64_t rows, int64_t cols, const void* dy, int64_t
   const bool params = dgamma || dbeta;
   const int64_t need = params ? bwd_workspace(rows, cols, dtype) : 0;
   if (params) {
-    if (workspace_bytes < 0) return fail(TRT_ERR_SIZE, "workspace_bytes must be >= 0");
-    if (!workspace)
-      return fail(TRT_ERR_NULL, "this call needs a workspace of " + std::to_string(need) + " bytes");
-    if (workspace_bytes < need)
-      return fail(TRT_ERR_SIZE, "the workspace must hold at least " + std::to_string(need) + " bytes");
-    if (reinterpret_cast<uintptr_t>(workspace) & 15u)
-      return fail(TRT_ERR_ALIGN, "the workspace must be 16-byte aligned");
+    if (const trt_status s = trt::check_workspace(workspace, workspace_bytes, need); s != TRT_OK) return s;
   }
   const int64_t e = trt::elem_bytes(dtype), pe = trt::elem_bytes(param_dtype);
   const Buf bufs[] = {{"dx", dx, rows, cols, lddx, e},

@@ -1,0 +1,259 @@
+// xent.hpp -- the vocabulary head's softmax cross entropy without its logits:
+// what the GEMM kernels do around their products for it, and the small
+// kernels beside them, for gfx950.
+//
+//   z = X W^T (tokens x vocabulary),  lse_t = log sum_v exp z_tv,
+//   loss_t = lse_t - z_t,target
+//   g_tv = exp(z_tv - lse_t) (dloss_t + dlse_t) - [v = target_t] dloss_t
+//   dX = G W,  dW = G^T X
+//
+// Forward: the GEMM kernel's tile of z never leaves the registers.  Its
+// epilogue takes each row's maximum and sum of exp(z - maximum) over the
+// tile's columns, one pair per row and tile (8 bytes for 256 logits), and the
+// target's logit where the tile holds it; xent_combine_kernel joins a row's
+// pairs.  Backward, in pieces of the vocabulary: the same product again, whose
+// epilogue turns z into g in the registers and rounds it once to the inputs'
+// type; then the two products of that piece of G.  Bound by the matrix cores
+// from a few hundred tokens on, by reading W below.
+//
+// Tokens whose target is the ignored one take no part: xent_prep_kernel lists
+// the others, the products' row counts are read from device memory, and A's
+// rows are reached through that list, so a batch that is half prompt costs
+// half, and whatever X holds at an ignored token (NaN included) reaches
+// nothing.
+//
+// Roundings to 16 bits beside the results' own.  G: with s_t = max(|dloss_t|,
+// |dloss_t + dlse_t|) taken out, |g| <= 2, and the entry that dominates a row,
+// p_target - 1, loses nothing where p_target is small.  s_t comes back in
+// binary32: as a factor of dX's row, and for dW as c = max_t s_t on the whole
+// and s_t / c on X's rows -- exactly 1 for a mean or a sum, where no further
+// rounding happens; with weights that differ from token to token it rounds
+// X's rows once more.  binary16 would lose small probabilities (its smallest
+// value is 2^-24): G is held times 2^14 there, which keeps all its bits down to
+// p = 2^-28.
+#pragma once
+
+#include "gemm_dma.hpp"
+#include "xent_args.hpp"
+
+namespace trt {
+
+// A's rows through the list of live tokens (all rows in place without one).
+struct LiveRows {
+  const int32_t* list;
+  int32_t rows;
+  __device__ int operator()(int r) const { return r >= rows ? -1 : (list ? list[r] : r); }
+};
+
+// A value that is the same for the whole workgroup, in a scalar register: the
+// copies' descriptors are scalar arithmetic on it.
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+// Sets the problem's row count to the number of live tokens; false for the
+// workgroups past the last tile that leaves.
+template <int BM, class P>
+__device__ __forceinline__ bool live_rows(P& p) {
+  if (p.live) p.M = uniform(*p.live);
+  p.tiles_m = (p.M + BM - 1) / BM;
+  return (int)blockIdx.x < p.tiles_m * p.tiles_n;
+}
+
+// ---- the forward product's epilogue -----------------------------------------
+
+template <class TL_, bool PIPELINED>
+struct XentStats {
+  using Args = XentStatsArgs;
+  __device__ static bool begin(Args& p) { return live_rows<TL_::BM>(p); }
+  __device__ static LiveRows rows(const Args& p) { return {p.list, p.M}; }
+
+  // A lane holds, for each of its FM rows, FN runs of four columns; the four
+  // lanes l, l+16, l+32, l+48 share a row.  Row sums therefore take two
+  // exchanges, then LDS joins the waves side by side in the tile.
+  template <class TL, int DT>
+  __device__ __forceinline__ static void finish(const Args& p, f32x4 (&acc)[TL::FM][TL::FN],
+                                                char* lds, int m0, int n0, int t) {
+    const int lane = t & 63, wave = t >> 6;
+    f32x2* pairs = reinterpret_cast<f32x2*>(lds);   // [WN][BM]
+    const int wn = wave % TL::WN;
+    const int c0 = TL::owner_col(0, lane, wave);
+    if (n0 + TL::BN > p.N) {
+#pragma unroll
+      for (int j = 0; j < TL::FN; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (n0 + c0 + 16 * j + e >= p.N)
+#pragma unroll
+            for (int i = 0; i < TL::FM; ++i) acc[i][j][e] = -__builtin_inff();
+    }
+    int want[TL::FM];   // the target's column, from the lane's first one on
+#pragma unroll
+    for (int i = 0; i < TL::FM; ++i) {
+      const int m = m0 + TL::owner_row(4 * i * TL::FN, lane, wave);
+      int64_t w = -1;
+      if (m < p.M) w = p.target[p.list ? p.list[m] : m] - p.col0 - n0 - c0;
+      want[i] = w >= 0 && w < TL::BN ? (int)w : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < TL::FM; ++i) {
+      const int row = TL::owner_row(4 * i * TL::FN, lane, wave);
+      float top = -__builtin_inff();
+#pragma unroll
+      for (int j = 0; j < TL::FN; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = __builtin_fmaxf(top, acc[i][j][e]);
+      top = __builtin_fmaxf(top, __shfl_xor(top, 16));
+      top = __builtin_fmaxf(top, __shfl_xor(top, 32));
+      // a row of -inf only: exp(-inf - 0) = 0
+      const float base = top == -__builtin_inff() ? 0.f : -top * kLog2E;
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < TL::FN; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          sum += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][e], kLog2E, base));
+          if (want[i] == 16 * j + e) p.at[m0 + row] = acc[i][j][e];
+        }
+      sum += __shfl_xor(sum, 16);
+      sum += __shfl_xor(sum, 32);
+      if (lane < 16) pairs[wn * TL::BM + row] = f32x2{top, sum};
+    }
+    __syncthreads();
+    if (t < TL::BM && m0 + t < p.M) {
+      float top = -__builtin_inff();
+#pragma unroll
+      for (int w = 0; w < TL::WN; ++w) top = __builtin_fmaxf(top, pairs[w * TL::BM + t][0]);
+      const float base = top == -__builtin_inff() ? 0.f : top;
+      float sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < TL::WN; ++w) {
+        const f32x2 q = pairs[w * TL::BM + t];
+        sum += q[1] * __builtin_amdgcn_exp2f((q[0] - base) * kLog2E);
+      }
+      p.part[(int64_t)(p.tile0 + n0 / TL::BN) * p.ldp + m0 + t] = f32x2{top, sum};
+    }
+  }
+};
+
+// ---- the backward products' epilogues -----------------------------------------
+
+// Stores a tile of the pipelined kernel, `fast` as in epilogue_lds.
+template <class TL, int OT, bool ADD>
+__device__ __forceinline__ void store_tile(const GemmArgs& p, const f32x4 (&acc)[TL::FM][TL::FN],
+                                           char* lds, int m0, int n0, int t, bool fast) {
+  float none[EpiShape<TL>::PANELS][4];
+#pragma unroll
+  for (int q = 0; q < EpiShape<TL>::PANELS; ++q)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) none[q][e] = -0.f;
+  float* stage = reinterpret_cast<float*>(lds);
+  if (fast) epilogue_passes<TL, OT, ADD ? EPI_FAST_RES : EPI_FAST>(p, acc, stage, m0, n0, t, none);
+  else epilogue_passes<TL, OT, EPI_MASKED>(p, acc, stage, m0, n0, t, none);
+}
+
+template <class TL_, bool PIPELINED>
+struct XentGrad {
+  using Args = XentGradArgs;
+  __device__ static bool begin(Args& p) { return live_rows<TL_::BM>(p); }
+  __device__ static LiveRows rows(const Args& p) { return {p.list, p.M}; }
+
+  template <class TL, int DT>
+  __device__ __forceinline__ static void finish(const Args& p, f32x4 (&acc)[TL::FM][TL::FN],
+                                                char* lds, int m0, int n0, int t) {
+    const int lane = t & 63, wave = t >> 6;
+    const int c0 = n0 + TL::owner_col(0, lane, wave);
+    XentRow q[TL::FM];
+#pragma unroll
+    for (int i = 0; i < TL::FM; ++i) {
+      const int m = m0 + TL::owner_row(4 * i * TL::FN, lane, wave);
+      q[i] = m < p.M ? p.info[m] : XentRow{0.f, 0.f, 0.f, -1};
+    }
+#pragma unroll
+    for (int i = 0; i < TL::FM; ++i) {
+      const float a = q[i].a * kGradScale<DT>, b = q[i].b * kGradScale<DT>;
+      const int64_t rel = (int64_t)q[i].target - p.col0 - c0;
+      const int want = rel >= 0 && rel < TL::BN ? (int)rel : -1;
+#pragma unroll
+      for (int j = 0; j < TL::FN; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float g = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][e], kLog2E, -q[i].lse2)) * a;
+          if (want == 16 * j + e) g -= b;
+          acc[i][j][e] = g;
+        }
+    }
+    if (n0 + TL::BN > p.cols) {
+#pragma unroll
+      for (int j = 0; j < TL::FN; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (c0 + 16 * j + e >= p.cols)
+#pragma unroll
+            for (int i = 0; i < TL::FM; ++i) acc[i][j][e] = 0.f;
+    }
+    // G's rows and N are whole vector runs
+    if constexpr (PIPELINED) store_tile<TL, DT, false>(p, acc, lds, m0, n0, t, true);
+    else epilogue_store<TL>(p, acc, m0, n0, lane, wave);
+  }
+};
+
+// dX += G W over one piece: binary32 sums in the workspace, one buffer for
+// each of the slices that K is cut into where rows are few (grid.y).
+template <class TL_, bool PIPELINED>
+struct XentInput {
+  using Args = XentInputArgs;
+  __device__ static bool begin(Args& p) {
+    const int64_t k0 = (int64_t)blockIdx.y * p.slice;
+    p.A += k0;
+    p.a_bytes = (int64_t)(p.M - 1) * p.lda * 2 + (p.K - k0) * 2;
+    p.B += k0 * p.ldb;
+    p.b_bytes -= k0 * p.ldb * 2;
+    p.K = p.K - k0 < p.slice ? p.K - (int)k0 : p.slice;
+    p.C = static_cast<float*>(p.C) + blockIdx.y * p.slice_stride;
+    p.R = p.add ? p.C : nullptr;
+    return live_rows<TL_::BM>(p);
+  }
+  __device__ static SameRows rows(const Args&) { return {}; }
+  template <class TL, int DT>
+  __device__ __forceinline__ static void finish(const Args& p, f32x4 (&acc)[TL::FM][TL::FN],
+                                                char* lds, int m0, int n0, int t) {
+    if constexpr (PIPELINED) {
+      // in place: a thread reads just the elements that it stores
+      if (p.add) store_tile<TL, DT_F32, true>(p, acc, lds, m0, n0, t, true);
+      else store_tile<TL, DT_F32, false>(p, acc, lds, m0, n0, t, true);
+    } else {
+      epilogue_store<TL>(p, acc, m0, n0, t & 63, t >> 6);
+    }
+  }
+};
+
+// dW = c G^T X' over the live tokens: K is their number.
+template <class TL_, bool PIPELINED>
+struct XentWeight {
+  using Args = XentWeightArgs;
+  __device__ static bool begin(Args& p) {
+    p.K = uniform(*p.live);
+    // in 32 bits: below 2^31 where the pipelined kernel runs, and only it asks
+    const int rows = p.K > 0 ? p.K - 1 : 0;
+    p.a_bytes = uniform((rows * (int)p.lda + p.g_cols) * 2);
+    p.b_bytes = uniform(p.K * (int)p.ldb * 2);
+    return true;
+  }
+  __device__ static SameRows rows(const Args&) { return {}; }
+  template <class TL, int DT>
+  __device__ __forceinline__ static void finish(const Args& p, f32x4 (&acc)[TL::FM][TL::FN],
+                                                char* lds, int m0, int n0, int t) {
+    const float f = *p.factor;
+#pragma unroll
+    for (int i = 0; i < TL::FM; ++i)
+#pragma unroll
+      for (int j = 0; j < TL::FN; ++j) acc[i][j] *= f;
+    if constexpr (PIPELINED) {
+      const bool fast = p.epi_vec && (n0 + TL::BN <= p.N || p.N % 4 == 0) && p.ldc < kEpiFastMaxLd;
+      with_out_type(p.out_dt, [&]<int OT>() { store_tile<TL, OT, false>(p, acc, lds, m0, n0, t, fast); });
+    } else {
+      epilogue_store<TL>(p, acc, m0, n0, t & 63, t >> 6);
+    }
+  }
+};
+
+}  // namespace trt

@@ -1,0 +1,196 @@
+// xent_rows.hpp -- the cross entropy's small kernels: the list of live tokens,
+// the join of a row's pairs, X' and dX's last step.  xent.hpp has the whole
+// picture.
+#pragma once
+
+#include "rowchunk.hpp"
+#include "xent_args.hpp"
+
+namespace trt {
+
+// The list of live tokens, in order, by one workgroup: each thread counts 8
+// tokens of a block of 8192, waves scan their threads' counts by shuffles and
+// the workgroup its waves' through LDS.  Backward, a token whose upstream
+// gradients are both zero is not live either, and the kernel takes c, the
+// largest s_t.  Forward, it writes the ignored tokens' results.
+constexpr int kPrepThreads = 1024, kPrepEach = 8;
+
+__device__ __forceinline__ float xent_weight(const XentPrepArgs& a, int64_t t, float& dl, float& both) {
+  dl = a.dloss[t * a.inc_dloss];
+  both = a.dlse ? dl + a.dlse[t * a.inc_dlse] : dl;
+  return __builtin_fmaxf(__builtin_fabsf(dl), __builtin_fabsf(both));
+}
+
+__global__ __launch_bounds__(kPrepThreads) void xent_prep_kernel(XentPrepArgs a) {
+  __shared__ int count[16];
+  __shared__ float top[16];
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  int base = 0;
+  float c = 0.f;
+  for (int64_t t0 = 0; t0 < a.tokens; t0 += kPrepThreads * kPrepEach) {
+    const int64_t first = t0 + (int64_t)t * kPrepEach;
+    uint32_t keep = 0;
+#pragma unroll
+    for (int e = 0; e < kPrepEach; ++e)
+      if (first + e < a.tokens && a.target[first + e] != a.ignore) {
+        float s = 1.f;
+        if (a.dloss) {
+          float dl, both;
+          s = xent_weight(a, first + e, dl, both);
+          c = __builtin_fmaxf(c, s);
+        }
+        if (s != 0.f) keep |= 1u << e;
+      }
+    int upto = __popc(keep);   // inclusive count over the wave's lanes
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int v = __shfl_up(upto, off);
+      if (lane >= off) upto += v;
+    }
+    if (lane == 63) count[wave] = upto;
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) {
+      before += w < wave ? count[w] : 0;
+      all += count[w];
+    }
+    int at = base + before + upto - __popc(keep);
+#pragma unroll
+    for (int e = 0; e < kPrepEach; ++e) {
+      const int64_t tok = first + e;
+      if (tok >= a.tokens) break;
+      const bool live = (keep >> e) & 1u;
+      if (a.place) a.place[tok] = live ? at : -1;
+      if (live) {
+        a.list[at++] = (int32_t)tok;
+      } else if (a.loss) {
+        a.loss[tok] = 0.f;
+        a.lse[tok] = 0.f;
+      }
+    }
+    base += all;
+    __syncthreads();
+  }
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) c = __builtin_fmaxf(c, __shfl_xor(c, off));
+  if (lane == 0) top[wave] = c;
+  __syncthreads();
+  if (t == 0) {
+    for (int w = 1; w < 16; ++w) c = __builtin_fmaxf(c, top[w]);
+    a.head->live = base;
+    a.head->c = c;
+    a.head->factor = c / a.scale;
+  }
+}
+
+// Joins a row's pairs: a workgroup of 256 threads takes R rows, 256 / R
+// threads to a row, thread j of them the tiles j, j + 256 / R, ...
+template <int R>
+__global__ __launch_bounds__(256) void xent_combine_kernel(XentCombineArgs a) {
+  constexpr int EACH = 256 / R;
+  __shared__ f32x2 pairs[EACH][R];
+  const int r = threadIdx.x % R, j = threadIdx.x / R;
+  const int rows = a.head ? a.head->live : a.tokens;
+  const int64_t m = (int64_t)blockIdx.x * R + r;
+  if ((int64_t)blockIdx.x * R >= rows) return;   // the whole workgroup
+  float top = -__builtin_inff(), sum = 0.f;
+  auto join = [&](f32x2 q) {
+    const float up = __builtin_fmaxf(top, q[0]);
+    const float base = up == -__builtin_inff() ? 0.f : up;
+    sum = sum * __builtin_amdgcn_exp2f((top - base) * kLog2E) +
+          q[1] * __builtin_amdgcn_exp2f((q[0] - base) * kLog2E);
+    top = up;
+  };
+  if (m < rows) {
+    const f32x2* p = a.part + m;
+#pragma unroll 4
+    for (int i = j; i < a.tiles; i += EACH) join(p[(int64_t)i * a.ldp]);
+  }
+  pairs[j][r] = f32x2{top, sum};
+  __syncthreads();
+#pragma unroll
+  for (int half = EACH / 2; half >= 1; half >>= 1) {
+    if (j < half) {
+      join(pairs[j + half][r]);
+      pairs[j][r] = f32x2{top, sum};
+    }
+    __syncthreads();
+  }
+  if (j != 0 || m >= rows) return;
+  const int64_t tok = a.list ? a.list[m] : m;
+  const int64_t target = a.target[tok];
+  const float rest = logf(sum);
+  if (target == a.ignore) {
+    a.loss[tok] = 0.f;
+    a.lse[tok] = 0.f;
+    return;
+  }
+  // a target outside the vocabulary has no loss: NaN, where it can be seen
+  const bool known = target >= 0 && target < a.vocab;
+  a.loss[tok] = known ? (top - a.at[m]) + rest : __builtin_nanf("");
+  a.lse[tok] = top + rest;
+}
+
+// The live tokens' rows: X' = X s_t / c, packed with a row of `ld` elements
+// (zero past the width), and what the gradient's epilogue needs of each.
+template <int DT>
+__global__ __launch_bounds__(256) void xent_rows_kernel(XentRowsArgs a) {
+  using C = RowChunk<DT>;
+  const int m = blockIdx.x;
+  if (m >= a.prep.head->live) return;   // the whole workgroup
+  const int tok = a.prep.list[m];
+  float dl, both;
+  const float s = xent_weight(a.prep, tok, dl, both);   // not zero: the token is live
+  const float c = a.prep.head->c;
+  const float ratio = s == c ? 1.f : s / c;   // exactly 1 for equal weights
+  if (threadIdx.x == 0) {
+    const int64_t target = a.prep.target[tok];
+    const bool known = target >= 0 && target < a.vocab;
+    // a target outside the vocabulary: a NaN row, where it can be seen.  The
+    // quotients are exactly 1 or -1 without a dlse
+    a.info[m] = XentRow{known ? both / s : __builtin_nanf(""), dl / s, a.lse[tok] * kLog2E,
+                        known ? (int32_t)target : -1};
+    a.weight[m] = s / a.prep.scale;
+  }
+  const uint16_t* src = a.x + (int64_t)tok * a.ldx;
+  uint16_t* dst = a.out + (int64_t)m * a.ld;
+  for (int i = C::VEC * threadIdx.x; i < a.ld; i += C::VEC * 256) {
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if (i < a.width) v = C::load(src, i, a.width);
+    if (ratio != 1.f) {
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+        v[w] = pack2_f32<DT>(C::elem(v, 2 * w) * ratio, C::elem(v, 2 * w + 1) * ratio);
+    }
+    *reinterpret_cast<u32x4*>(dst + i) = v;
+  }
+}
+
+// dX from the slices' sums: row t is its weight times the sum over the slices
+// in order, or zeros for an ignored token.
+template <int OT>
+__global__ __launch_bounds__(256) void xent_input_finish_kernel(XentInputFinishArgs a) {
+  using C = RowChunk<OT>;
+  const int64_t t = blockIdx.x;
+  const int m = a.place[t];
+  const float w = m < 0 ? 0.f : a.weight[m];
+  void* row = static_cast<typename C::Elem*>(a.dx) + t * a.lddx;
+  for (int i = C::VEC * threadIdx.x; i < a.width; i += C::VEC * 256) {
+    float v[C::VEC];
+#pragma unroll
+    for (int q = 0; q < C::VEC; q += 4) {   // the sums' rows are padded to whole eights
+      f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+      if (m >= 0) {
+        const float* p = a.sums + (int64_t)m * a.ld + i + q;
+        sum = *reinterpret_cast<const f32x4*>(p);
+        for (int s = 1; s < a.slices; ++s) sum += *reinterpret_cast<const f32x4*>(p + s * a.slice_stride);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[q + e] = m < 0 ? 0.f : sum[e] * w;
+    }
+    C::store(row, i, a.width, v);
+  }
+}
+
+}  // namespace trt
