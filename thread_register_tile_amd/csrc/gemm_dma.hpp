@@ -620,15 +620,21 @@ struct FragReader {
 // What a kernel does around the product: the GEMM's own epilogue here, the
 // cross entropy's in xent.hpp.  Args extends GemmArgs; begin(p) may narrow the
 // problem from device memory or the grid's second axis (false: the workgroup
-// has no tile); rows(p) maps A's rows to stored ones; finish() takes the
-// tile's accumulators, with every LDS stage free for its use.
+// has no tile); rows(p) maps A's rows to stored ones; fetch() may issue copies
+// of what finish() needs into KEPT bytes of LDS (a multiple of 1 KiB) ahead of
+// the operands'; finish() takes the tile's accumulators, with every LDS stage
+// free for its use and the kept bytes behind them.
 struct GemmEpilogue {
   using Args = GemmArgs;
+  template <class TL>
+  static constexpr int KEPT = 0;
+  template <class TL>
+  __device__ static void fetch(const Args&, uint32_t, int, int, int) {}
   __device__ static bool begin(Args&) { return true; }
   __device__ static SameRows rows(const Args&) { return {}; }
   template <class TL, int DT>
   __device__ __forceinline__ static void finish(const Args& p, f32x4 (&acc)[TL::FM][TL::FN],
-                                                char* lds, int m0, int n0, int t) {
+                                                char* lds, char*, int m0, int n0, int t) {
     with_out_type(p.out_dt, [&]<int OT>() {
       epilogue_lds<TL, OT>(p, acc, reinterpret_cast<float*>(lds), m0, n0, t);
     });
@@ -656,7 +662,8 @@ __global__ __launch_bounds__(TL::THREADS, 1) void gemm_dma_kernel(typename EPI::
   constexpr int EPI_BYTES = (BM / 2) * BN * 4;
   constexpr int LDS_BYTES = NS * STAGE > EPI_BYTES ? NS * STAGE : EPI_BYTES;
   static_assert(FM % 2 == 0 && HALF >= 2, "copies fit the first half");
-  __shared__ __attribute__((aligned(1024))) char lds_raw[LDS_BYTES];
+  static_assert(EPI::template KEPT<TL> % 1024 == 0, "whole copies");
+  __shared__ __attribute__((aligned(1024))) char lds_raw[LDS_BYTES + EPI::template KEPT<TL>];
   TRT_LDS char* lds = (TRT_LDS char*)lds_raw;
 
   const int t = threadIdx.x;
@@ -711,6 +718,8 @@ __global__ __launch_bounds__(TL::THREADS, 1) void gemm_dma_kernel(typename EPI::
   const int r = nk % NS;
   auto stage_of = [&](int s) { return (uint32_t)((s - r + NS) % NS) * STAGE; };
 
+  // (the oldest copies: complete once the first step's are)
+  EPI::template fetch<TL>(p, lds_base + LDS_BYTES, m0, wave, lane);
   // prologue: steps 0..NS-2 in flight, step 0's fragments in registers
 #pragma unroll
   for (int step = 0; step < NS - 1; ++step) {
@@ -798,7 +807,7 @@ __global__ __launch_bounds__(TL::THREADS, 1) void gemm_dma_kernel(typename EPI::
   __builtin_amdgcn_s_waitcnt(waitcnt_lgkm(0));
   __syncthreads();
 
-  EPI::template finish<TL, DT>(p, acc, lds_raw, m0, n0, t);
+  EPI::template finish<TL, DT>(p, acc, lds_raw, lds_raw + LDS_BYTES, m0, n0, t);
 }
 
 }  // namespace trt

@@ -481,7 +481,7 @@ struct GenericEpilogue {
   __device__ static SameRows rows(const Args&) { return {}; }
   template <class TL, int DT>
   __device__ __forceinline__ static void finish(const Args& p, f32x4 (&acc)[TL::FM][TL::FN],
-                                                char*, int m0, int n0, int t) {
+                                                char*, char*, int m0, int n0, int t) {
     epilogue_store<TL>(p, acc, m0, n0, t & 63, t >> 6);
   }
 };
@@ -567,7 +567,7 @@ __global__ __launch_bounds__(TL::THREADS) void gemm_kernel(typename EPI::Args p)
     __syncthreads();
   }
 
-  EPI::template finish<TL, DT>(p, acc, reinterpret_cast<char*>(lds), m0, n0, t);
+  EPI::template finish<TL, DT>(p, acc, reinterpret_cast<char*>(lds), nullptr, m0, n0, t);
 }
 
 }  // namespace trt

@@ -2,6 +2,7 @@
 // included only by the kern_xent*.hip units, one product each.
 #pragma once
 
+#include "gemm_wide.hpp"
 #include "launch.hpp"
 #include "tiles.hpp"
 #include "xent.hpp"
@@ -15,14 +16,19 @@ hipError_t launch_xent_tile(Args a, int dt, int slices, hipStream_t s) {
   a.tiles_m = (a.M + TL::BM - 1) / TL::BM;
   a.tiles_n = (a.N + TL::BN - 1) / TL::BN;
   const dim3 grid(a.tiles_m * a.tiles_n, slices), block(TL::THREADS);
-  if (dt == DT_F16) return launch(gemm_dma_kernel<TL, DT_F16, A_KC, B_KC, 4, EPI>, grid, block, 0, s, a);
-  return launch(gemm_dma_kernel<TL, DT_BF16, A_KC, B_KC, 4, EPI>, grid, block, 0, s, a);
+  if constexpr (TL::BM == 256) {
+    if (dt == DT_F16) return launch(gemm_wide_kernel<TL, DT_F16, A_KC, B_KC, EPI>, grid, block, 0, s, a);
+    return launch(gemm_wide_kernel<TL, DT_BF16, A_KC, B_KC, EPI>, grid, block, 0, s, a);
+  } else {
+    if (dt == DT_F16) return launch(gemm_dma_kernel<TL, DT_F16, A_KC, B_KC, 4, EPI>, grid, block, 0, s, a);
+    return launch(gemm_dma_kernel<TL, DT_BF16, A_KC, B_KC, 4, EPI>, grid, block, 0, s, a);
+  }
 }
 
 template <template <class, bool> class EPI_OF, bool A_KC, bool B_KC, class Args>
 hipError_t launch_xent_product(Args a, int dt, bool wide, bool pipelined, int slices, hipStream_t s) {
   if (pipelined)
-    return wide ? launch_xent_tile<EPI_OF, Tile256D, A_KC, B_KC>(a, dt, slices, s)
+    return wide ? launch_xent_tile<EPI_OF, Tile256F, A_KC, B_KC>(a, dt, slices, s)
                 : launch_xent_tile<EPI_OF, Tile128D, A_KC, B_KC>(a, dt, slices, s);
   using EPI = EPI_OF<Tile128, false>;
   a.tiles_m = (a.M + Tile128::BM - 1) / Tile128::BM;

@@ -78,6 +78,7 @@ trt_status trt_linear_xent(int64_t tokens, int64_t vocab, int64_t width, const v
   const bool listed = tokens > trt::kXentInPlace;
   auto* head = reinterpret_cast<trt::XentHead*>(ws + plan.head);
   auto* list = reinterpret_cast<int32_t*>(ws + plan.list);
+  auto* want = reinterpret_cast<int32_t*>(ws + plan.want);
   hipError_t e = hipSuccess;
   if (listed) {
     trt::XentPrepArgs a{};
@@ -87,6 +88,8 @@ trt_status trt_linear_xent(int64_t tokens, int64_t vocab, int64_t width, const v
     a.loss = loss;
     a.lse = lse;
     a.list = list;
+    a.want = want;
+    a.vocab = (int32_t)vocab;
     a.head = head;
     a.scale = 1.f;
     e = trt::launch_xent_prep(a, st);
@@ -113,6 +116,7 @@ trt_status trt_linear_xent(int64_t tokens, int64_t vocab, int64_t width, const v
     a.b_bytes = ((n - 1) * ldw + width) * 2;
     a.live = listed ? &head->live : nullptr;
     a.list = listed ? list : nullptr;
+    a.want = listed ? want : nullptr;
     a.target = target;
     a.at = reinterpret_cast<float*>(ws + plan.at);
     a.part = reinterpret_cast<trt::f32x2*>(ws + plan.part);
@@ -308,6 +312,7 @@ trt_status trt_linear_xent_bwd(int64_t tokens, int64_t vocab, int64_t width, con
     f.lddx = lddx;
     f.slices = (int32_t)plan.slices;
     f.width = (int32_t)width;
+    f.vec = (reinterpret_cast<uintptr_t>(dx) & (uintptr_t)(4 * oe - 1)) == 0 && lddx % 4 == 0;
     return done(trt::launch_xent_input_finish(f, tokens, out_dtype, st));
   }
   return done(hipSuccess);

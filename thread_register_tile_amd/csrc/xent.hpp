@@ -49,6 +49,37 @@ struct LiveRows {
 // copies' descriptors are scalar arithmetic on it.
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
+// Copies 1 KiB of an array of `rows` entries of `each` bytes, from entry m0 on,
+// to LDS address lds (one wave); 16-byte words past the last entry's read as
+// zero.  (A descriptor drops a copy that its end cuts, so the end is rounded
+// up: the arrays are padded in the workspace.)
+__device__ __forceinline__ void copy_rows(const void* base, int rows, int each, uint32_t lds,
+                                          int m0, int lane) {
+  const auto rs = __builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0, (rows * each + 15) & ~15,
+                                                    kBufferFormat);
+  dma16(rs, uniform((int)lds), (uint32_t)(m0 * each + 16 * lane));
+}
+
+// Maximum and sum over the four lanes l, l + 16, l + 32, l + 48 that share a
+// row of a fragment, in each of them.  Exchanging the odd rows of 16 lanes (then
+// the upper 32 lanes) of a value with the even ones (lower 32) of its copy
+// leaves both halves' values side by side in every lane.
+template <class F>
+__device__ __forceinline__ float over_row(float v, F&& f) {
+  const uint32_t u = __float_as_uint(v);
+  const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  v = f(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  const uint32_t w = __float_as_uint(v);
+  const auto b = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+  return f(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ __forceinline__ float row_max(float v) {
+  return over_row(v, [](float a, float b) { return __builtin_fmaxf(a, b); });
+}
+__device__ __forceinline__ float row_sum(float v) {
+  return over_row(v, [](float a, float b) { return a + b; });
+}
+
 // Sets the problem's row count to the number of live tokens; false for the
 // workgroups past the last tile that leaves.
 template <int BM, class P>
@@ -65,13 +96,20 @@ struct XentStats {
   using Args = XentStatsArgs;
   __device__ static bool begin(Args& p) { return live_rows<TL_::BM>(p); }
   __device__ static LiveRows rows(const Args& p) { return {p.list, p.M}; }
+  // the tile's targets, 4 bytes a row
+  template <class TL>
+  static constexpr int KEPT = 1024;
+  template <class TL>
+  __device__ static void fetch(const Args& p, uint32_t lds, int m0, int wave, int lane) {
+    if (p.want && wave == 0) copy_rows(p.want, p.M, 4, lds, m0, lane);
+  }
 
   // A lane holds, for each of its FM rows, FN runs of four columns; the four
   // lanes l, l+16, l+32, l+48 share a row.  Row sums therefore take two
   // exchanges, then LDS joins the waves side by side in the tile.
   template <class TL, int DT>
   __device__ __forceinline__ static void finish(const Args& p, f32x4 (&acc)[TL::FM][TL::FN],
-                                                char* lds, int m0, int n0, int t) {
+                                                char* lds, char* kept, int m0, int n0, int t) {
     const int lane = t & 63, wave = t >> 6;
     f32x2* pairs = reinterpret_cast<f32x2*>(lds);   // [WN][BM]
     const int wn = wave % TL::WN;
@@ -85,37 +123,47 @@ struct XentStats {
 #pragma unroll
             for (int i = 0; i < TL::FM; ++i) acc[i][j][e] = -__builtin_inff();
     }
-    int want[TL::FM];   // the target's column, from the lane's first one on
 #pragma unroll
     for (int i = 0; i < TL::FM; ++i) {
-      const int m = m0 + TL::owner_row(4 * i * TL::FN, lane, wave);
-      int64_t w = -1;
-      if (m < p.M) w = p.target[p.list ? p.list[m] : m] - p.col0 - n0 - c0;
-      want[i] = w >= 0 && w < TL::BN ? (int)w : -1;
-    }
-#pragma unroll
-    for (int i = 0; i < TL::FM; ++i) {
-      const int row = TL::owner_row(4 * i * TL::FN, lane, wave);
-      float top = -__builtin_inff();
+      float v[4 * TL::FN];
 #pragma unroll
       for (int j = 0; j < TL::FN; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) top = __builtin_fmaxf(top, acc[i][j][e]);
-      top = __builtin_fmaxf(top, __shfl_xor(top, 16));
-      top = __builtin_fmaxf(top, __shfl_xor(top, 32));
+        for (int e = 0; e < 4; ++e) v[4 * j + e] = acc[i][j][e];
+      float top = v[0];
+#pragma unroll
+      for (int c = 1; c + 1 < 4 * TL::FN; c += 2) top = __builtin_fmaxf(__builtin_fmaxf(top, v[c]), v[c + 1]);
+      top = row_max(__builtin_fmaxf(top, v[4 * TL::FN - 1]));
       // a row of -inf only: exp(-inf - 0) = 0
       const float base = top == -__builtin_inff() ? 0.f : -top * kLog2E;
-      float sum = 0.f;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int j = 0; j < TL::FN; ++j)
+      for (int c = 0; c < 4 * TL::FN; ++c)
+        sum[c & 3] += __builtin_amdgcn_exp2f(__builtin_fmaf(v[c], kLog2E, base));
+      const float all = row_sum((sum[0] + sum[1]) + (sum[2] + sum[3]));
+      if (lane < 16) pairs[wn * TL::BM + TL::owner_row(4 * i * TL::FN, lane, wave)] = f32x2{top, all};
+    }
+    // the targets' columns, from the lane's first one on; few waves hold any
+    int want[TL::FM];
+    bool any = false;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          sum += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][e], kLog2E, base));
-          if (want[i] == 16 * j + e) p.at[m0 + row] = acc[i][j][e];
-        }
-      sum += __shfl_xor(sum, 16);
-      sum += __shfl_xor(sum, 32);
-      if (lane < 16) pairs[wn * TL::BM + row] = f32x2{top, sum};
+    for (int i = 0; i < TL::FM; ++i) {
+      const int row = TL::owner_row(4 * i * TL::FN, lane, wave), m = m0 + row;
+      int64_t v = -1;
+      if (PIPELINED && p.want) v = reinterpret_cast<const int32_t*>(kept)[row];
+      else if (m < p.M) v = p.want ? p.want[m] : p.target[m];
+      v -= p.col0 + n0 + c0;
+      want[i] = m < p.M && v >= 0 && v < 16 * TL::FN ? (int)v : -1;
+      any |= want[i] >= 0;
+    }
+    if (__any(any)) {
+#pragma unroll
+      for (int i = 0; i < TL::FM; ++i)
+#pragma unroll
+        for (int j = 0; j < TL::FN; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (want[i] == 16 * j + e) p.at[m0 + TL::owner_row(4 * i * TL::FN, lane, wave)] = acc[i][j][e];
     }
     __syncthreads();
     if (t < TL::BM && m0 + t < p.M) {
@@ -155,31 +203,40 @@ struct XentGrad {
   using Args = XentGradArgs;
   __device__ static bool begin(Args& p) { return live_rows<TL_::BM>(p); }
   __device__ static LiveRows rows(const Args& p) { return {p.list, p.M}; }
+  // the tile's row entries, 64 to a wave's copy
+  template <class TL>
+  static constexpr int KEPT = TL::BM * (int)sizeof(XentRow);
+  template <class TL>
+  __device__ static void fetch(const Args& p, uint32_t lds, int m0, int wave, int lane) {
+    static_assert(sizeof(XentRow) == 16 && TL::BM / 64 <= TL::WAVES, "one copy a wave");
+    if (wave < TL::BM / 64) copy_rows(p.info, p.M, 16, lds + 1024 * wave, m0 + 64 * wave, lane);
+  }
 
   template <class TL, int DT>
   __device__ __forceinline__ static void finish(const Args& p, f32x4 (&acc)[TL::FM][TL::FN],
-                                                char* lds, int m0, int n0, int t) {
+                                                char* lds, char* kept, int m0, int n0, int t) {
     const int lane = t & 63, wave = t >> 6;
     const int c0 = n0 + TL::owner_col(0, lane, wave);
-    XentRow q[TL::FM];
 #pragma unroll
     for (int i = 0; i < TL::FM; ++i) {
-      const int m = m0 + TL::owner_row(4 * i * TL::FN, lane, wave);
-      q[i] = m < p.M ? p.info[m] : XentRow{0.f, 0.f, 0.f, -1};
-    }
-#pragma unroll
-    for (int i = 0; i < TL::FM; ++i) {
-      const float a = q[i].a * kGradScale<DT>, b = q[i].b * kGradScale<DT>;
-      const int64_t rel = (int64_t)q[i].target - p.col0 - c0;
-      const int want = rel >= 0 && rel < TL::BN ? (int)rel : -1;
+      const int row = TL::owner_row(4 * i * TL::FN, lane, wave), m = m0 + row;
+      XentRow q = {0.f, 0.f, 0.f, -1};
+      if constexpr (PIPELINED) q = reinterpret_cast<const XentRow*>(kept)[row];
+      else if (m < p.M) q = p.info[m];
+      const float a = q.a * kGradScale<DT>, b = q.b * kGradScale<DT>;
 #pragma unroll
       for (int j = 0; j < TL::FN; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float g = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][e], kLog2E, -q[i].lse2)) * a;
-          if (want == 16 * j + e) g -= b;
-          acc[i][j][e] = g;
-        }
+        for (int e = 0; e < 4; ++e)
+          acc[i][j][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][e], kLog2E, -q.lse2)) * a;
+      const int64_t rel = (int64_t)q.target - p.col0 - c0;
+      const int want = rel >= 0 && rel < 16 * TL::FN ? (int)rel : -1;
+      if (__any(want >= 0)) {   // few waves hold any of their rows' targets
+#pragma unroll
+        for (int j = 0; j < TL::FN; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][j][e] -= want == 16 * j + e ? b : 0.f;
+      }
     }
     if (n0 + TL::BN > p.cols) {
 #pragma unroll
@@ -213,9 +270,13 @@ struct XentInput {
     return live_rows<TL_::BM>(p);
   }
   __device__ static SameRows rows(const Args&) { return {}; }
+  template <class TL>
+  static constexpr int KEPT = 0;
+  template <class TL>
+  __device__ static void fetch(const Args&, uint32_t, int, int, int) {}
   template <class TL, int DT>
   __device__ __forceinline__ static void finish(const Args& p, f32x4 (&acc)[TL::FM][TL::FN],
-                                                char* lds, int m0, int n0, int t) {
+                                                char* lds, char*, int m0, int n0, int t) {
     if constexpr (PIPELINED) {
       // in place: a thread reads just the elements that it stores
       if (p.add) store_tile<TL, DT_F32, true>(p, acc, lds, m0, n0, t, true);
@@ -239,9 +300,13 @@ struct XentWeight {
     return true;
   }
   __device__ static SameRows rows(const Args&) { return {}; }
+  template <class TL>
+  static constexpr int KEPT = 0;
+  template <class TL>
+  __device__ static void fetch(const Args&, uint32_t, int, int, int) {}
   template <class TL, int DT>
   __device__ __forceinline__ static void finish(const Args& p, f32x4 (&acc)[TL::FM][TL::FN],
-                                                char* lds, int m0, int n0, int t) {
+                                                char* lds, char*, int m0, int n0, int t) {
     const float f = *p.factor;
 #pragma unroll
     for (int i = 0; i < TL::FM; ++i)

@@ -17,6 +17,7 @@ constexpr float kGradScale = DT == DT_F16 ? 16384.f : 1.f;
 struct XentStatsArgs : GemmArgs {
   const int32_t* live;     // number of live tokens, or null: all M
   const int32_t* list;     // their rows in X, or null: in place
+  const int32_t* want;     // the live tokens' targets, or null: target in place
   const int64_t* target;   // [tokens]
   float* at;               // [M] the target's logit
   f32x2* part;             // [tiles_n][tokens] (maximum, sum of exp(z - maximum))
@@ -63,6 +64,8 @@ struct XentPrepArgs {
   int64_t inc_dloss, inc_dlse;
   float *loss, *lse;           // forward, else null
   int32_t *list, *place;       // live token -> row of X; row -> live token or -1 (backward)
+  int32_t* want;               // forward: the live tokens' targets, -1 outside the vocabulary
+  int32_t vocab;
   XentHead* head;
   float scale;                 // backward: G's scale
 };
@@ -97,6 +100,7 @@ struct XentInputFinishArgs {
   void* dx;
   int64_t ld, slice_stride, lddx;
   int32_t slices, width;
+  int32_t vec;             // dx's rows take aligned runs of four
 };
 
 // pipelined: the operands allow 16-byte copies; otherwise the generic kernel

@@ -28,7 +28,7 @@ constexpr int64_t kXentInPlace = 128;
 
 struct XentFwdPlan {
   bool wide;           // 256x256 tiles, else 128x128
-  int64_t part, at, list, head;   // byte offsets into the workspace
+  int64_t part, at, list, want, head;   // byte offsets into the workspace
   int64_t bytes;
 };
 
@@ -47,6 +47,7 @@ constexpr XentFwdPlan xent_fwd_plan(int64_t tokens, int64_t vocab) {
   p.part = take((vocab + 127) / 128 * tokens * 8);   // for either tile
   p.at = take(tokens * 4);
   p.list = take(tokens > kXentInPlace ? tokens * 4 : 0);
+  p.want = take(tokens > kXentInPlace ? tokens * 4 : 0);
   p.bytes = at;
   return p;
 }

@@ -63,6 +63,10 @@ __global__ __launch_bounds__(kPrepThreads) void xent_prep_kernel(XentPrepArgs a)
       const bool live = (keep >> e) & 1u;
       if (a.place) a.place[tok] = live ? at : -1;
       if (live) {
+        if (a.want) {
+          const int64_t v = a.target[tok];
+          a.want[at] = v >= 0 && v < a.vocab ? (int32_t)v : -1;
+        }
         a.list[at++] = (int32_t)tok;
       } else if (a.loss) {
         a.loss[tok] = 0.f;
@@ -171,25 +175,27 @@ __global__ __launch_bounds__(256) void xent_rows_kernel(XentRowsArgs a) {
 // in order, or zeros for an ignored token.
 template <int OT>
 __global__ __launch_bounds__(256) void xent_input_finish_kernel(XentInputFinishArgs a) {
-  using C = RowChunk<OT>;
+  using O = Out<OT>;
   const int64_t t = blockIdx.x;
   const int m = a.place[t];
   const float w = m < 0 ? 0.f : a.weight[m];
-  void* row = static_cast<typename C::Elem*>(a.dx) + t * a.lddx;
-  for (int i = C::VEC * threadIdx.x; i < a.width; i += C::VEC * 256) {
-    float v[C::VEC];
-#pragma unroll
-    for (int q = 0; q < C::VEC; q += 4) {   // the sums' rows are padded to whole eights
-      f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-      if (m >= 0) {
-        const float* p = a.sums + (int64_t)m * a.ld + i + q;
-        sum = *reinterpret_cast<const f32x4*>(p);
-        for (int s = 1; s < a.slices; ++s) sum += *reinterpret_cast<const f32x4*>(p + s * a.slice_stride);
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[q + e] = m < 0 ? 0.f : sum[e] * w;
+  for (int i = 4 * threadIdx.x; i < a.width; i += 1024) {
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    if (m >= 0) {   // the sums' rows are padded to whole eights
+      const float* p = a.sums + (int64_t)m * a.ld + i;
+#pragma unroll 8
+      for (int s = 0; s < a.slices; ++s) v += *reinterpret_cast<const f32x4*>(p + s * a.slice_stride);
+      v *= w;
     }
-    C::store(row, i, a.width, v);
+    const int64_t at = t * a.lddx + i;
+    if (a.vec && i + 4 <= a.width) {
+      const float y[4] = {v[0], v[1], v[2], v[3]};
+      O::st4(a.dx, at, O::pack(y));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (i + e < a.width) O::st(a.dx, at + e, v[e]);
+    }
   }
 }
 
