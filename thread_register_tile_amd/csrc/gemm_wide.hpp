@@ -23,6 +23,11 @@
 //   second half: the products of set 1, reading step kt + 1's first fragments
 //     into set 0, with the copies of step kt + 2 into the free stage between
 //     the products.
+//
+// An epilogue that leaves the stages alone (EPI::STREAMS) runs on a grid of one
+// workgroup per compute unit that walks the tiles: the copies of the next
+// tile's first two steps go out ahead of the epilogue, which covers their
+// latency and the gap between two workgroups.
 #pragma once
 
 #include "gemm_dma.hpp"
@@ -47,11 +52,14 @@ __device__ __forceinline__ void accumulators_done() {
 }
 
 // One 16-byte copy per lane to LDS address m0v + OFF + 16 * lane (see
-// dma_block: the instruction offset is added on both sides).
-template <int OFF>
+// dma_block: the instruction offset is added on both sides).  The main loop's
+// descriptors are scalar arithmetic on loop-carried registers; elsewhere a
+// descriptor word may come from a vector instruction (a restored scalar), and
+// the copy waits out the five states itself (NOPS = 4).
+template <int OFF, int NOPS>
 __device__ __forceinline__ void dma_one(__amdgpu_buffer_rsrc_t rs, uint32_t m0v, uint32_t v) {
-  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen offset:%3 lds"
-               :: "{m0}"(m0v), "v"(v), "s"(rs), "n"(OFF));
+  asm volatile("s_nop %4\n\tbuffer_load_dwordx4 %1, %2, 0 offen offset:%3 lds"
+               :: "{m0}"(m0v), "v"(v), "s"(rs), "n"(OFF), "n"(NOPS));
 }
 
 // Swizzle of a k-contiguous stage, rows of 8 chunks: chunk (r, g) in slot
@@ -84,17 +92,27 @@ struct WideOperand {
   static_assert(R * 8 % TL::THREADS == 0 && NCH == 8, "two M0 values, four instruction offsets");
 
   const char* cur;
-  uint32_t rem, step_bytes;
+  uint32_t rem, step_bytes;   // step_bytes: rows-contiguous
   uint32_t voff[NCH];
   uint32_t drop;          // k-contiguous: bit i, copy i lies past K on the last step
 
-  template <class Rows>
-  __device__ __forceinline__ void init(const uint16_t* X, int64_t ld, int64_t ext, int row0,
-                                       int wave, int lane, int K, Rows rows) {
-    cur = reinterpret_cast<const char*>(X) - BIAS;
-    rem = (uint32_t)ext + BIAS;
+  // What every tile shares.
+  __device__ __forceinline__ void setup(int64_t ld, int wave, int lane, int K) {
+    step_bytes = (uint32_t)(128 * ld);
     drop = 0;
     const int last = (K + 63) / 64 * 64 - 64;
+#pragma unroll
+    for (int i = 0; KC && i < NCH; ++i) {
+      const int s = (wave * NCH + i) * 64 + lane, g = (s & 7) ^ wide_swz(s >> 3);
+      drop |= last + 8 * g >= K ? 1u << i : 0u;
+    }
+  }
+
+  template <class Rows>
+  __device__ __forceinline__ void init(const uint16_t* X, int64_t ld, int64_t ext, int row0,
+                                       int wave, int lane, Rows rows) {
+    cur = reinterpret_cast<const char*>(X) - BIAS;
+    rem = (uint32_t)ext + BIAS;
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
       const int s = (wave * NCH + i) * 64 + lane;
@@ -105,7 +123,6 @@ struct WideOperand {
         off = (uint32_t)(((int64_t)row * ld + 8 * g) * 2);
         if constexpr (!std::is_same_v<Rows, SameRows>)
           if (row < 0) off = 0x80000000u;   // beyond every record count
-        drop |= last + 8 * g >= K ? 1u << i : 0u;
       } else {
         const int h = s / (4 * R), u = s % (4 * R);
         const int k = 32 * h + TL::template mn_slot_k<R>(u), c = TL::template mn_slot_c<R>(u);
@@ -113,7 +130,6 @@ struct WideOperand {
       }
       voff[i] = off + BIAS - 1024u * (i & 3);
     }
-    step_bytes = (uint32_t)(KC ? 128 : 128 * ld);
   }
 
   // Copy I of K step `step` of nk to the wave's slots at m0v; CHECKED as in
@@ -127,10 +143,11 @@ struct WideOperand {
       if (KC && step == nk - 1) v |= (drop >> I) << 31;
     }
     const auto rs = __builtin_amdgcn_make_buffer_rsrc((void*)cur, (short)0, records, kBufferFormat);
-    dma_one<1024 * (I & 3)>(rs, m0v + 4096u * (I >> 2), v);
+    dma_one<1024 * (I & 3), CHECKED ? 4 : 0>(rs, m0v + 4096u * (I >> 2), v);
     if constexpr (I == NCH - 1) {
-      cur += step_bytes;
-      rem -= step_bytes;
+      const uint32_t bytes = KC ? 128 : step_bytes;
+      cur += bytes;
+      rem -= bytes;
     }
   }
 };
@@ -175,34 +192,45 @@ struct WideReader {
   }
 };
 
+// Workgroups of a grid that walks its tiles: one for each compute unit.
+constexpr int kWideUnits = 256;
+
+template <class EPI, class TL>
+constexpr int wide_scratch() {
+  if constexpr (EPI::STREAMS) return EPI::template SCRATCH<TL>;
+  else return 0;
+}
+
 template <class TL, int DT, bool A_KC, bool B_KC, class EPI>
 __global__ __launch_bounds__(TL::THREADS, 1) void gemm_wide_kernel(typename EPI::Args p) {
   static_assert(TL::MF == 16 && TL::WAVES == 4, "four waves, 16x16x32 fragments");
   constexpr int BM = TL::BM, BN = TL::BN, FM = TL::FM, FN = TL::FN;
   constexpr int PRODUCTS = FM * FN, READS = FM + FN;
+  using Args = typename EPI::Args;
   using OpA = WideOperand<TL, BM, A_KC>;
   using OpB = WideOperand<TL, BN, B_KC>;
   constexpr int STAGE = OpA::BYTES + OpB::BYTES;
   constexpr int COPIES = OpA::NCH + OpB::NCH;
   static_assert(3 * READS <= PRODUCTS && 4 * COPIES <= PRODUCTS, "reads and copies fit between the products");
-  constexpr int EPI_BYTES = (BM / 2) * BN * 4;
+  constexpr int EPI_BYTES = EPI::STREAMS ? 0 : (BM / 2) * BN * 4;
   constexpr int LDS_BYTES = 2 * STAGE > EPI_BYTES ? 2 * STAGE : EPI_BYTES;
-  static_assert(EPI::template KEPT<TL> % 1024 == 0, "whole copies");
-  __shared__ __attribute__((aligned(1024))) char lds_raw[LDS_BYTES + EPI::template KEPT<TL>];
+  constexpr int KEPT = EPI::template KEPT<TL>;
+  static_assert(KEPT % 1024 == 0, "whole copies");
+  // behind the stages: what the epilogue keeps (of this tile and the next),
+  // and its scratch
+  constexpr int KEPT_BYTES = EPI::STREAMS ? 2 * KEPT : KEPT;
+  constexpr int SCRATCH = wide_scratch<EPI, TL>();
+  __shared__ __attribute__((aligned(1024))) char lds_raw[LDS_BYTES + KEPT_BYTES + SCRATCH];
   TRT_LDS char* lds = (TRT_LDS char*)lds_raw;
 
   const int t = threadIdx.x;
   const int lane = t & 63, wave = t >> 6;
   if (!EPI::begin(p)) return;
-  int tm, tn;
-  tile_of<8>(blockIdx.x, p.tiles_m, p.tiles_n, tm, tn);
-  const int m0 = tm * BM, n0 = tn * BN;
 
   OpA a;
   OpB b;
-  a.init(p.A, p.lda, p.a_bytes, m0, wave, lane, p.K, EPI::rows(p));
-  b.init(p.B, p.ldb, p.b_bytes, n0, wave, lane, p.K, SameRows{});
-
+  a.setup(p.lda, wave, lane, p.K);
+  b.setup(p.ldb, wave, lane, p.K);
   const int nk = (p.K + 63) / 64;
   const uint32_t lds_base = (uint32_t)(uintptr_t)lds;
   const uint32_t m0a = __builtin_amdgcn_readfirstlane(lds_base + wave * OpA::NCH * 1024);
@@ -215,18 +243,13 @@ __global__ __launch_bounds__(TL::THREADS, 1) void gemm_wide_kernel(typename EPI:
   rb.init(TL::owner_col(0, 0, wave), lane, OpA::BYTES);
 
   f32x4 acc[FM][FN];
-#pragma unroll
-  for (int i = 0; i < FM; ++i)
-#pragma unroll
-    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-
   u32x4 fa[2][FM], fb[2][FN];
   // fragment f of half HALF of the step in stage STG, into set HALF
   auto read_frag = [&]<int STG, int HALF, int F>() __attribute__((always_inline)) {
     if constexpr (F < FM) fa[HALF][F] = ra.template read<STG, HALF>(lds, F);
     else fb[HALF][F - FM] = rb.template read<STG, HALF>(lds, F - FM);
   };
-  auto copy = [&]<bool CHECKED, int C>(int step, uint32_t st) __attribute__((always_inline)) {
+  auto copy = [&]<bool CHECKED, int C>(int step, int nk, uint32_t st) __attribute__((always_inline)) {
     if constexpr (C < OpA::NCH) a.template copy<CHECKED, C>(step, nk, m0a + st);
     else b.template copy<CHECKED, C - OpA::NCH>(step, nk, m0b + st);
   };
@@ -234,17 +257,45 @@ __global__ __launch_bounds__(TL::THREADS, 1) void gemm_wide_kernel(typename EPI:
     (f.template operator()<I>(), ...);
   };
 
-  // prologue: steps 0 and 1 in flight, step 0's first fragments in registers
-  EPI::template fetch<TL>(p, lds_base + LDS_BYTES, m0, wave, lane);
-  each([&]<int C>() __attribute__((always_inline)) { copy.template operator()<true, C>(0, 0); },
-       std::make_integer_sequence<int, COPIES>{});
-  each([&]<int C>() __attribute__((always_inline)) { copy.template operator()<true, C>(1, STAGE); },
-       std::make_integer_sequence<int, COPIES>{});
-  __builtin_amdgcn_s_waitcnt(waitcnt_vm(COPIES));
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-  each([&]<int F>() __attribute__((always_inline)) { read_frag.template operator()<0, 0, F>(); },
-       std::make_integer_sequence<int, READS>{});
+  // The arguments, read again where they are needed (a tile's start and its
+  // epilogue): kept, they would hold scalar registers through the main loop,
+  // and a scalar spilled to a vector register may not feed a copy (dma_block).
+  // Of what begin() changed, a streaming epilogue's is M and the tile rows.
+  const int live_m = p.M, tiles_m = p.tiles_m;
+  auto arguments = [&]() __attribute__((always_inline)) {
+    typedef const __attribute__((address_space(4))) uint64_t* Words;
+    static_assert(sizeof(Args) % 8 == 0 && alignof(Args) == 8, "whole words");
+    Words from = (Words)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(from));
+    uint64_t words[sizeof(Args) / 8];
+#pragma unroll
+    for (size_t i = 0; i < sizeof(Args) / 8; ++i) words[i] = from[i];
+    Args q = __builtin_bit_cast(Args, words);
+    q.M = live_m;
+    q.tiles_m = tiles_m;
+    return q;
+  };
+
+  // A tile's first copies: what the epilogue keeps, steps 0 and 1.
+  int m0 = 0, n0 = 0;
+  auto enter = [&](const Args& p, int tile, int turn) __attribute__((always_inline)) {
+    int tm, tn;
+    tile_of<8>(tile, p.tiles_m, p.tiles_n, tm, tn);
+    m0 = tm * BM;
+    n0 = tn * BN;
+    // (the lane as a value of this tile's own: nothing made of it is kept from
+    // tile to tile, where it would hold registers through the main loop)
+    int l = lane, steps = nk;
+    asm volatile("" : "+v"(l));
+    asm volatile("" : "+s"(steps));
+    a.init(p.A, p.lda, p.a_bytes, m0, wave, l, EPI::rows(p));
+    b.init(p.B, p.ldb, p.b_bytes, n0, wave, l, SameRows{});
+    EPI::template fetch<TL>(p, lds_base + LDS_BYTES + turn * KEPT, m0, wave, l);
+    each([&]<int C>() __attribute__((always_inline)) { copy.template operator()<true, C>(0, steps, 0); },
+         std::make_integer_sequence<int, COPIES>{});
+    each([&]<int C>() __attribute__((always_inline)) { copy.template operator()<true, C>(1, steps, STAGE); },
+         std::make_integer_sequence<int, COPIES>{});
+  };
 
   // Step kt, whose stage is U = kt mod 2.
   auto step_body = [&]<bool CHECKED, int U>(int kt) __attribute__((always_inline)) {
@@ -265,31 +316,62 @@ __global__ __launch_bounds__(TL::THREADS, 1) void gemm_wide_kernel(typename EPI:
       mfma16_acc<DT>(acc[i][j], fb[1][j], fa[1][i]);
       __builtin_amdgcn_sched_barrier(0);
       if constexpr (Q % 3 == 0 && Q / 3 < READS) read_frag.template operator()<U ^ 1, 0, Q / 3>();
-      if constexpr (Q % 4 == 1 && Q / 4 < COPIES) copy.template operator()<CHECKED, Q / 4>(kt + 2, U * STAGE);
+      if constexpr (Q % 4 == 1 && Q / 4 < COPIES) copy.template operator()<CHECKED, Q / 4>(kt + 2, nk, U * STAGE);
       __builtin_amdgcn_sched_barrier(0);
     }, std::make_integer_sequence<int, PRODUCTS>{});
   };
 
-  // Whole rounds of two steps; all but the last two copy live steps before
-  // the last one only.
-  int kt = 0;
-  for (; kt + 4 < nk; kt += 2) {
-    step_body.template operator()<false, 0>(kt);
-    step_body.template operator()<false, 1>(kt + 1);
-  }
-  for (; kt + 2 <= nk; kt += 2) {
-    step_body.template operator()<true, 0>(kt);
-    step_body.template operator()<true, 1>(kt + 1);
-  }
-  if (kt < nk) step_body.template operator()<true, 0>(kt);
-  // drain the copies issued past the end (zero records: they fetch nothing)
-  // and the reads of the stage after the last
-  __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
-  __builtin_amdgcn_s_waitcnt(waitcnt_lgkm(0));
-  accumulators_done();
-  __syncthreads();
+  int tile = blockIdx.x, turn = 0;
+  if constexpr (EPI::STREAMS) enter(arguments(), tile, turn);
+  else enter(p, tile, turn);
+  for (;;) {
+    // step 0's copies are older than the 16 youngest operations in any case
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(COPIES));
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    each([&]<int F>() __attribute__((always_inline)) { read_frag.template operator()<0, 0, F>(); },
+         std::make_integer_sequence<int, READS>{});
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  EPI::template finish<TL, DT>(p, acc, lds_raw, lds_raw + LDS_BYTES, m0, n0, t);
+    // Whole rounds of two steps; all but the last two copy live steps before
+    // the last one only.
+    int kt = 0;
+    for (; kt + 4 < nk; kt += 2) {
+      step_body.template operator()<false, 0>(kt);
+      step_body.template operator()<false, 1>(kt + 1);
+    }
+    for (; kt + 2 <= nk; kt += 2) {
+      step_body.template operator()<true, 0>(kt);
+      step_body.template operator()<true, 1>(kt + 1);
+    }
+    if (kt < nk) step_body.template operator()<true, 0>(kt);
+    // drain the copies issued past the end (zero records: they fetch nothing)
+    // and the reads of the stage after the last
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+    __builtin_amdgcn_s_waitcnt(waitcnt_lgkm(0));
+    accumulators_done();
+    __syncthreads();
+
+    char* kept = lds_raw + LDS_BYTES + turn * KEPT;
+    if constexpr (EPI::STREAMS) {
+      const int em = m0, en = n0;
+      tile += kWideUnits;
+      turn ^= 1;
+      const Args q = arguments();
+      const bool more = tile < q.tiles_m * q.tiles_n;
+      if (more) enter(arguments(), tile, turn);
+      int et = t;
+      asm volatile("" : "+v"(et));
+      EPI::template finish<TL, DT>(q, acc, lds_raw + LDS_BYTES + KEPT_BYTES, kept, em, en, et);
+      if (!more) return;
+    } else {
+      EPI::template finish<TL, DT>(p, acc, lds_raw, kept, m0, n0, t);
+      return;
+    }
+  }
 }
 
 }  // namespace trt

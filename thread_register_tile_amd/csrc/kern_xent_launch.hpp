@@ -17,6 +17,9 @@ hipError_t launch_xent_tile(Args a, int dt, int slices, hipStream_t s) {
   a.tiles_n = (a.N + TL::BN - 1) / TL::BN;
   const dim3 grid(a.tiles_m * a.tiles_n, slices), block(TL::THREADS);
   if constexpr (TL::BM == 256) {
+    // one workgroup per compute unit walks the tiles, or one per tile
+    const int tiles = a.tiles_m * a.tiles_n;
+    const dim3 grid(EPI::STREAMS && tiles > kWideUnits ? kWideUnits : tiles, slices);
     if (dt == DT_F16) return launch(gemm_wide_kernel<TL, DT_F16, A_KC, B_KC, EPI>, grid, block, 0, s, a);
     return launch(gemm_wide_kernel<TL, DT_BF16, A_KC, B_KC, EPI>, grid, block, 0, s, a);
   } else {

@@ -38,11 +38,17 @@
 
 namespace trt {
 
-// A's rows through the list of live tokens (all rows in place without one).
+// A's rows through the list of live tokens (ALWAYS: there is one; else all rows
+// in place without one).  rows > 0.
+template <bool ALWAYS>
 struct LiveRows {
   const int32_t* list;
   int32_t rows;
-  __device__ int operator()(int r) const { return r >= rows ? -1 : (list ? list[r] : r); }
+  __device__ int operator()(int r) const {
+    int at = r;
+    if (ALWAYS || list) at = list[r < rows ? r : rows - 1];
+    return r < rows ? at : -1;
+  }
 };
 
 // A value that is the same for the whole workgroup, in a scalar register: the
@@ -57,7 +63,9 @@ __device__ __forceinline__ void copy_rows(const void* base, int rows, int each, 
                                           int m0, int lane) {
   const auto rs = __builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0, (rows * each + 15) & ~15,
                                                     kBufferFormat);
-  dma16(rs, uniform((int)lds), (uint32_t)(m0 * each + 16 * lane));
+  // (five wait states after whatever wrote the descriptor: see dma_one)
+  asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :: "{m0}"(uniform((int)lds)), "v"((uint32_t)(m0 * each + 16 * lane)), "s"(rs));
 }
 
 // Maximum and sum over the four lanes l, l + 16, l + 32, l + 48 that share a
@@ -95,13 +103,20 @@ template <class TL_, bool PIPELINED>
 struct XentStats {
   using Args = XentStatsArgs;
   __device__ static bool begin(Args& p) { return live_rows<TL_::BM>(p); }
-  __device__ static LiveRows rows(const Args& p) { return {p.list, p.M}; }
+  static constexpr bool LISTED = TL_::BM == 256;   // tiles of 128 serve few tokens too, in place
+  __device__ static LiveRows<LISTED> rows(const Args& p) { return {p.list, p.M}; }
+  // finish() needs 8 bytes of LDS for each row and wave beside it
+  static constexpr bool STREAMS = true;
+  template <class TL>
+  static constexpr int SCRATCH = TL::WN * TL::BM * 8;
   // the tile's targets, 4 bytes a row
   template <class TL>
   static constexpr int KEPT = 1024;
   template <class TL>
   __device__ static void fetch(const Args& p, uint32_t lds, int m0, int wave, int lane) {
-    if (p.want && wave == 0) copy_rows(p.want, p.M, 4, lds, m0, lane);
+    // (by every wave, the same bytes to the same place: a branch on the wave
+    // costs more)
+    if (LISTED || p.want) copy_rows(p.want, p.M, 4, lds, m0, lane);
   }
 
   // A lane holds, for each of its FM rows, FN runs of four columns; the four
@@ -114,56 +129,52 @@ struct XentStats {
     f32x2* pairs = reinterpret_cast<f32x2*>(lds);   // [WN][BM]
     const int wn = wave % TL::WN;
     const int c0 = TL::owner_col(0, lane, wave);
-    if (n0 + TL::BN > p.N) {
+    auto rows = [&]<bool EDGE>() __attribute__((always_inline)) {
 #pragma unroll
-      for (int j = 0; j < TL::FN; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (n0 + c0 + 16 * j + e >= p.N)
-#pragma unroll
-            for (int i = 0; i < TL::FM; ++i) acc[i][j][e] = -__builtin_inff();
-    }
-#pragma unroll
-    for (int i = 0; i < TL::FM; ++i) {
-      float v[4 * TL::FN];
-#pragma unroll
-      for (int j = 0; j < TL::FN; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[4 * j + e] = acc[i][j][e];
-      float top = v[0];
-#pragma unroll
-      for (int c = 1; c + 1 < 4 * TL::FN; c += 2) top = __builtin_fmaxf(__builtin_fmaxf(top, v[c]), v[c + 1]);
-      top = row_max(__builtin_fmaxf(top, v[4 * TL::FN - 1]));
-      // a row of -inf only: exp(-inf - 0) = 0
-      const float base = top == -__builtin_inff() ? 0.f : -top * kLog2E;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int c = 0; c < 4 * TL::FN; ++c)
-        sum[c & 3] += __builtin_amdgcn_exp2f(__builtin_fmaf(v[c], kLog2E, base));
-      const float all = row_sum((sum[0] + sum[1]) + (sum[2] + sum[3]));
-      if (lane < 16) pairs[wn * TL::BM + TL::owner_row(4 * i * TL::FN, lane, wave)] = f32x2{top, all};
-    }
-    // the targets' columns, from the lane's first one on; few waves hold any
-    int want[TL::FM];
-    bool any = false;
-#pragma unroll
-    for (int i = 0; i < TL::FM; ++i) {
-      const int row = TL::owner_row(4 * i * TL::FN, lane, wave), m = m0 + row;
-      int64_t v = -1;
-      if (PIPELINED && p.want) v = reinterpret_cast<const int32_t*>(kept)[row];
-      else if (m < p.M) v = p.want ? p.want[m] : p.target[m];
-      v -= p.col0 + n0 + c0;
-      want[i] = m < p.M && v >= 0 && v < 16 * TL::FN ? (int)v : -1;
-      any |= want[i] >= 0;
-    }
-    if (__any(any)) {
-#pragma unroll
-      for (int i = 0; i < TL::FM; ++i)
+      for (int i = 0; i < TL::FM; ++i) {
+        int left = p.N - n0 - c0;   // columns from the lane's first one on
+        // (made anew for each row: the 32 comparisons with it, kept from row
+        // to row, would take 64 scalar registers)
+        asm volatile("" : "+v"(left));
+        float v[4 * TL::FN];
 #pragma unroll
         for (int j = 0; j < TL::FN; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (want[i] == 16 * j + e) p.at[m0 + TL::owner_row(4 * i * TL::FN, lane, wave)] = acc[i][j][e];
+            v[4 * j + e] = EDGE && 16 * j + e >= left ? -__builtin_inff() : acc[i][j][e];
+        float top = v[0];
+#pragma unroll
+        for (int c = 1; c + 1 < 4 * TL::FN; c += 2) top = __builtin_fmaxf(__builtin_fmaxf(top, v[c]), v[c + 1]);
+        top = row_max(__builtin_fmaxf(top, v[4 * TL::FN - 1]));
+        // a row of -inf only: exp(-inf - 0) = 0
+        const float base = top == -__builtin_inff() ? 0.f : -top * kLog2E;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 4 * TL::FN; ++c)
+          sum[c & 3] += __builtin_amdgcn_exp2f(__builtin_fmaf(v[c], kLog2E, base));
+        const float all = row_sum((sum[0] + sum[1]) + (sum[2] + sum[3]));
+        if (lane < 16) pairs[wn * TL::BM + TL::owner_row(4 * i * TL::FN, lane, wave)] = f32x2{top, all};
+      }
+    };
+    if (n0 + TL::BN > p.N) rows.template operator()<true>();
+    else rows.template operator()<false>();
+    // the targets' columns, from the lane's first one on; few waves hold any
+#pragma unroll
+    for (int i = 0; i < TL::FM; ++i) {
+      const int row = TL::owner_row(4 * i * TL::FN, lane, wave), m = m0 + row;
+      int64_t v = -1;
+      if (PIPELINED && (LISTED || p.want)) v = reinterpret_cast<const int32_t*>(kept)[row];
+      else if (m < p.M) v = p.want ? p.want[m] : p.target[m];
+      v -= p.col0 + n0 + c0;
+      const int want = m < p.M && v >= 0 && v < 16 * TL::FN && (v & 15) < 4 ? (int)v : -1;
+      if (__any(want >= 0)) {
+        float at = 0.f;
+#pragma unroll
+        for (int j = 0; j < TL::FN; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) at = want == 16 * j + e ? acc[i][j][e] : at;
+        if (want >= 0) p.at[m] = at;
+      }
     }
     __syncthreads();
     if (t < TL::BM && m0 + t < p.M) {
@@ -198,18 +209,61 @@ __device__ __forceinline__ void store_tile(const GemmArgs& p, const f32x4 (&acc)
   else epilogue_passes<TL, OT, EPI_MASKED>(p, acc, stage, m0, n0, t, none);
 }
 
+// Stores a tile of 16-bit elements straight from the accumulators.  A lane
+// holds four columns of a row in each fragment; exchanging them between the
+// lanes 16 apart over two neighbouring fragments gives each lane eight
+// consecutive columns of one fragment, 16 bytes.  The four stores that fill a
+// 128-byte line follow each other, and the L2 joins them.  C through a descriptor
+// that ends at row M; N and ldc are multiples of 8 and C is 16-byte aligned.
+template <class TL, int DT>
+__device__ __forceinline__ void store_rows(const GemmArgs& p, const f32x4 (&acc)[TL::FM][TL::FN],
+                                           int m0, int n0, int lane, int wave) {
+  const int rows = p.M - m0 < TL::BM ? p.M - m0 : TL::BM;
+  const auto rs = __builtin_amdgcn_make_buffer_rsrc(
+      (void*)(static_cast<uint16_t*>(p.C) + (int64_t)m0 * p.ldc), (short)0,
+      (int)((uint32_t)rows * (uint32_t)p.ldc * 2u), kBufferFormat);
+  const int odd = (lane >> 4) & 1;
+  // after the exchange: columns of fragment 2 jj + odd, from its run 2 (lane / 32) on
+  const int c0 = n0 + TL::owner_col(0, 0, wave) + 16 * odd + 8 * (lane >> 5);
+  static_assert(TL::FN % 2 == 0, "fragments in pairs");
+#pragma unroll
+  for (int i = 0; i < TL::FM; ++i) {
+    const uint32_t row = (uint32_t)TL::owner_row(4 * i * TL::FN, lane, wave) * (uint32_t)p.ldc;
+#pragma unroll
+    for (int j = 0; j < TL::FN; j += 2) {
+      u32x4 v;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t lo = pack2_f32<DT>(acc[i][j][2 * h], acc[i][j][2 * h + 1]);
+        const uint32_t hi = pack2_f32<DT>(acc[i][j + 1][2 * h], acc[i][j + 1][2 * h + 1]);
+        const auto x = __builtin_amdgcn_permlane16_swap(lo, hi, false, false);
+        v[h] = x[0];
+        v[2 + h] = x[1];
+      }
+      const int c = c0 + 16 * j;
+      const uint32_t off = (row + (uint32_t)c) * 2u | (c < p.N ? 0u : 0x80000000u);
+      __builtin_amdgcn_raw_buffer_store_b128(v, rs, (int)off, 0, 0);
+    }
+  }
+}
+
 template <class TL_, bool PIPELINED>
 struct XentGrad {
   using Args = XentGradArgs;
   __device__ static bool begin(Args& p) { return live_rows<TL_::BM>(p); }
-  __device__ static LiveRows rows(const Args& p) { return {p.list, p.M}; }
+  __device__ static LiveRows<true> rows(const Args& p) { return {p.list, p.M}; }
+  // finish() needs no LDS
+  static constexpr bool STREAMS = true;
+  template <class TL>
+  static constexpr int SCRATCH = 0;
   // the tile's row entries, 64 to a wave's copy
   template <class TL>
   static constexpr int KEPT = TL::BM * (int)sizeof(XentRow);
   template <class TL>
   __device__ static void fetch(const Args& p, uint32_t lds, int m0, int wave, int lane) {
-    static_assert(sizeof(XentRow) == 16 && TL::BM / 64 <= TL::WAVES, "one copy a wave");
-    if (wave < TL::BM / 64) copy_rows(p.info, p.M, 16, lds + 1024 * wave, m0 + 64 * wave, lane);
+    static_assert(sizeof(XentRow) == 16 && TL::WAVES % (TL::BM / 64) == 0, "one copy a wave");
+    const int w = wave % (TL::BM / 64);
+    copy_rows(p.info, p.M, 16, lds + 1024 * w, m0 + 64 * w, lane);
   }
 
   template <class TL, int DT>
@@ -247,8 +301,7 @@ struct XentGrad {
 #pragma unroll
             for (int i = 0; i < TL::FM; ++i) acc[i][j][e] = 0.f;
     }
-    // G's rows and N are whole vector runs
-    if constexpr (PIPELINED) store_tile<TL, DT, false>(p, acc, lds, m0, n0, t, true);
+    if constexpr (PIPELINED) store_rows<TL, DT>(p, acc, m0, n0, lane, wave);
     else epilogue_store<TL>(p, acc, m0, n0, lane, wave);
   }
 };
@@ -270,6 +323,7 @@ struct XentInput {
     return live_rows<TL_::BM>(p);
   }
   __device__ static SameRows rows(const Args&) { return {}; }
+  static constexpr bool STREAMS = false;
   template <class TL>
   static constexpr int KEPT = 0;
   template <class TL>
@@ -300,6 +354,7 @@ struct XentWeight {
     return true;
   }
   __device__ static SameRows rows(const Args&) { return {}; }
+  static constexpr bool STREAMS = false;
   template <class TL>
   static constexpr int KEPT = 0;
   template <class TL>
