@@ -619,8 +619,8 @@ struct FragReader {
 
 // What a kernel does around the product: the GEMM's own epilogue here, the
 // cross entropy's in xent.hpp.  Args extends GemmArgs; begin(p) may narrow the
-// problem from device memory or the grid's second axis (false: the workgroup
-// has no tile); rows(p) maps A's rows to stored ones; fetch() may issue copies
+// problem from device memory (false: the workgroup has no tile); tile(p) is
+// the workgroup's place among the tiles; rows(p) maps A's rows to stored ones; fetch() may issue copies
 // of what finish() needs into KEPT bytes of LDS (a multiple of 1 KiB) ahead of
 // the operands'; finish() takes the tile's accumulators, with every LDS stage
 // free for its use and the kept bytes behind them.
@@ -631,6 +631,7 @@ struct GemmEpilogue {
   template <class TL>
   __device__ static void fetch(const Args&, uint32_t, int, int, int) {}
   __device__ static bool begin(Args&) { return true; }
+  __device__ static int tile(const Args&) { return blockIdx.x; }
   __device__ static SameRows rows(const Args&) { return {}; }
   template <class TL, int DT>
   __device__ __forceinline__ static void finish(const Args& p, f32x4 (&acc)[TL::FM][TL::FN],
@@ -670,7 +671,7 @@ __global__ __launch_bounds__(TL::THREADS, 1) void gemm_dma_kernel(typename EPI::
   const int lane = t & 63, wave = t >> 6;
   if (!EPI::begin(p)) return;
   int tm, tn;
-  tile_of<8>(blockIdx.x, p.tiles_m, p.tiles_n, tm, tn);
+  tile_of<8>(EPI::tile(p), p.tiles_m, p.tiles_n, tm, tn);
   const int m0 = tm * BM, n0 = tn * BN;
 
   OpA a;

@@ -478,6 +478,7 @@ __device__ __forceinline__ void epilogue_store(const GemmArgs& p,
 struct GenericEpilogue {
   using Args = GemmArgs;
   __device__ static bool begin(Args&) { return true; }
+  __device__ static int tile(const Args&) { return blockIdx.x; }
   __device__ static SameRows rows(const Args&) { return {}; }
   template <class TL, int DT>
   __device__ __forceinline__ static void finish(const Args& p, f32x4 (&acc)[TL::FM][TL::FN],
@@ -501,7 +502,7 @@ __global__ __launch_bounds__(TL::THREADS) void gemm_kernel(typename EPI::Args p)
   const int lane = t & 63, wave = t >> 6;
   if (!EPI::begin(p)) return;
   int tm, tn;
-  tile_of<8>(blockIdx.x, p.tiles_m, p.tiles_n, tm, tn);
+  tile_of<8>(EPI::tile(p), p.tiles_m, p.tiles_n, tm, tn);
   const int m0 = tm * TL::BM, n0 = tn * TL::BN;
   const bool full_mn = (m0 + TL::BM <= p.M) && (n0 + TL::BN <= p.N);
 

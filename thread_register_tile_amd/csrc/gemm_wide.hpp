@@ -321,7 +321,7 @@ __global__ __launch_bounds__(TL::THREADS, 1) void gemm_wide_kernel(typename EPI:
     }, std::make_integer_sequence<int, PRODUCTS>{});
   };
 
-  int tile = blockIdx.x, turn = 0;
+  int tile = EPI::tile(p), turn = 0;
   if constexpr (EPI::STREAMS) enter(arguments(), tile, turn);
   else enter(p, tile, turn);
   for (;;) {

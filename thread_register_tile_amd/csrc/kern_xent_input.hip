@@ -4,9 +4,9 @@
 
 namespace trt {
 
-hipError_t launch_xent_input(XentInputArgs a, int dt, bool wide, bool pipelined, int slices,
+hipError_t launch_xent_input(XentInputArgs a, int dt, bool wide, bool pipelined, int64_t groups,
                              hipStream_t s) {
-  return launch_xent_product<XentInput, true, false>(a, dt, wide, pipelined, slices, s);
+  return launch_xent_product<XentInput, true, false>(a, dt, wide, pipelined, groups, s);
 }
 
 }  // namespace trt

@@ -5,7 +5,7 @@
 namespace trt {
 
 hipError_t launch_xent_stats(XentStatsArgs a, int dt, bool wide, bool pipelined, hipStream_t s) {
-  return launch_xent_product<XentStats, true, true>(a, dt, wide, pipelined, 1, s);
+  return launch_xent_product<XentStats, true, true>(a, dt, wide, pipelined, 0, s);
 }
 
 }  // namespace trt

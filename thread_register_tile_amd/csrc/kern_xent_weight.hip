@@ -5,7 +5,7 @@
 namespace trt {
 
 hipError_t launch_xent_weight(XentWeightArgs a, int dt, bool wide, bool pipelined, hipStream_t s) {
-  return launch_xent_product<XentWeight, false, false>(a, dt, wide, pipelined, 1, s);
+  return launch_xent_product<XentWeight, false, false>(a, dt, wide, pipelined, 0, s);
 }
 
 }  // namespace trt

@@ -205,6 +205,9 @@ trt_status trt_linear_xent_bwd(int64_t tokens, int64_t vocab, int64_t width, con
   r.prep.place = place;
   r.prep.head = head;
   r.prep.scale = in_dtype == TRT_F16 ? trt::kGradScale<trt::DT_F16> : trt::kGradScale<trt::DT_BF16>;
+  r.prep.width = (int32_t)width;
+  r.prep.k = (int32_t)(plan.piece < vocab ? plan.piece : vocab);
+  r.prep.wide = plan.wide_x;
   r.x = static_cast<const uint16_t*>(x);
   r.out = xs;
   r.lse = lse;
@@ -288,29 +291,28 @@ trt_status trt_linear_xent_bwd(int64_t tokens, int64_t vocab, int64_t width, con
       b.out_dt = TRT_F32;
       b.epi_vec = 1;
       b.b_bytes = ((n - 1) * ldw + width) * 2;
-      b.live = &head->live;
-      b.slice = (int32_t)plan.slice;
+      b.head = head;
       b.add = v0 > 0;
-      b.slice_stride = tokens * plan.padded;
       // the pipelined kernel takes G's zero columns up to a multiple of 8 too,
       // where they are written; W's rows there lie past its extent and read as zero
       const bool pipelined = vec_w && vec_g && (grad_pipelined || n == n8);
       b.K = (int32_t)(pipelined ? n8 : n);
-      const int slices = (int)((b.K + plan.slice - 1) / plan.slice);
-      if (const hipError_t e = trt::launch_xent_input(b, in_dtype, plan.wide_x, pipelined, slices, st); e != hipSuccess)
+      // the grid holds the most workgroups that any number of live tokens asks
+      // for; on a tile of 128 for one of 256, four times as many
+      const int64_t groups = plan.most_tiles * (plan.wide_x && !pipelined ? 4 : 1);
+      if (const hipError_t e = trt::launch_xent_input(b, in_dtype, plan.wide_x, pipelined, groups, st); e != hipSuccess)
         return done(e);
     }
   }
   if (dx) {
     trt::XentInputFinishArgs f{};
     f.sums = sums;
+    f.head = head;
     f.place = place;
     f.weight = weight;
     f.dx = dx;
     f.ld = plan.padded;
-    f.slice_stride = tokens * plan.padded;
     f.lddx = lddx;
-    f.slices = (int32_t)plan.slices;
     f.width = (int32_t)width;
     f.vec = (reinterpret_cast<uintptr_t>(dx) & (uintptr_t)(4 * oe - 1)) == 0 && lddx % 4 == 0;
     return done(trt::launch_xent_input_finish(f, tokens, out_dtype, st));

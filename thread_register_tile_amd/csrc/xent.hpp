@@ -102,6 +102,7 @@ __device__ __forceinline__ bool live_rows(P& p) {
 template <class TL_, bool PIPELINED>
 struct XentStats {
   using Args = XentStatsArgs;
+  __device__ static int tile(const Args&) { return blockIdx.x; }
   __device__ static bool begin(Args& p) { return live_rows<TL_::BM>(p); }
   static constexpr bool LISTED = TL_::BM == 256;   // tiles of 128 serve few tokens too, in place
   __device__ static LiveRows<LISTED> rows(const Args& p) { return {p.list, p.M}; }
@@ -250,6 +251,7 @@ __device__ __forceinline__ void store_rows(const GemmArgs& p, const f32x4 (&acc)
 template <class TL_, bool PIPELINED>
 struct XentGrad {
   using Args = XentGradArgs;
+  __device__ static int tile(const Args&) { return blockIdx.x; }
   __device__ static bool begin(Args& p) { return live_rows<TL_::BM>(p); }
   __device__ static LiveRows<true> rows(const Args& p) { return {p.list, p.M}; }
   // finish() needs no LDS
@@ -307,21 +309,30 @@ struct XentGrad {
 };
 
 // dX += G W over one piece: binary32 sums in the workspace, one buffer for
-// each of the slices that K is cut into where rows are few (grid.y).
+// each of the slices that K is cut into where tiles are few (xent_plan.hpp).
 template <class TL_, bool PIPELINED>
 struct XentInput {
   using Args = XentInputArgs;
+  // Workgroups in order of their slice, then of their tile.
   __device__ static bool begin(Args& p) {
-    const int64_t k0 = (int64_t)blockIdx.y * p.slice;
+    const int slice = uniform(p.head->slice);
+    p.M = uniform(p.head->live);
+    p.tiles_m = (p.M + TL_::BM - 1) / TL_::BM;
+    const int tiles = p.tiles_m * p.tiles_n;
+    const int at = tiles > 0 ? blockIdx.x / (uint32_t)tiles : 0;
+    if (tiles == 0 || (int64_t)at * slice >= p.K) return false;
+    const int k0 = at * slice;
     p.A += k0;
-    p.a_bytes = (int64_t)(p.M - 1) * p.lda * 2 + (p.K - k0) * 2;
     p.B += k0 * p.ldb;
     p.b_bytes -= k0 * p.ldb * 2;
-    p.K = p.K - k0 < p.slice ? p.K - (int)k0 : p.slice;
-    p.C = static_cast<float*>(p.C) + blockIdx.y * p.slice_stride;
+    p.K = p.K - k0 < slice ? p.K - k0 : slice;
+    // (32 bits suffice where the pipelined kernel runs, and only it asks)
+    p.a_bytes = uniform(((p.M - 1) * (int)p.lda + p.K) * 2);
+    p.C = static_cast<float*>(p.C) + at * (xent_sum_rows(p.M) * p.ldc);
     p.R = p.add ? p.C : nullptr;
-    return live_rows<TL_::BM>(p);
+    return true;
   }
+  __device__ static int tile(const Args& p) { return (int)(blockIdx.x % (uint32_t)(p.tiles_m * p.tiles_n)); }
   __device__ static SameRows rows(const Args&) { return {}; }
   static constexpr bool STREAMS = false;
   template <class TL>
@@ -345,6 +356,7 @@ struct XentInput {
 template <class TL_, bool PIPELINED>
 struct XentWeight {
   using Args = XentWeightArgs;
+  __device__ static int tile(const Args&) { return blockIdx.x; }
   __device__ static bool begin(Args& p) {
     p.K = uniform(*p.live);
     // in 32 bits: below 2^31 where the pipelined kernel runs, and only it asks

@@ -43,10 +43,8 @@ struct XentGradArgs : GemmArgs {   // C: G, of the inputs' type
 
 // dX's sums over one piece.
 struct XentInputArgs : GemmArgs {
-  const int32_t* live;
-  int32_t slice;           // K of a slice, a multiple of 64
-  int32_t add;             // add to what the buffer holds (every piece after the first)
-  int64_t slice_stride;    // floats between the slices' buffers
+  const XentHead* head;
+  int32_t add;             // add to what the sums hold (every piece after the first)
 };
 
 // dW over one piece.
@@ -68,6 +66,7 @@ struct XentPrepArgs {
   int32_t vocab;
   XentHead* head;
   float scale;                 // backward: G's scale
+  int32_t width, k, wide;      // backward: dX's product, K of a whole piece
 };
 
 struct XentCombineArgs {
@@ -95,11 +94,12 @@ struct XentRowsArgs {
 
 struct XentInputFinishArgs {
   const float* sums;
+  const XentHead* head;
   const int32_t* place;
   const float* weight;
   void* dx;
-  int64_t ld, slice_stride, lddx;
-  int32_t slices, width;
+  int64_t ld, lddx;
+  int32_t width;
   int32_t vec;             // dx's rows take aligned runs of four
 };
 
@@ -107,7 +107,7 @@ struct XentInputFinishArgs {
 // on 128x128 tiles runs the same epilogue.
 hipError_t launch_xent_stats(XentStatsArgs a, int dt, bool wide, bool pipelined, hipStream_t s);
 hipError_t launch_xent_grad(XentGradArgs a, int dt, bool wide, bool pipelined, hipStream_t s);
-hipError_t launch_xent_input(XentInputArgs a, int dt, bool wide, bool pipelined, int slices,
+hipError_t launch_xent_input(XentInputArgs a, int dt, bool wide, bool pipelined, int64_t groups,
                              hipStream_t s);
 hipError_t launch_xent_weight(XentWeightArgs a, int dt, bool wide, bool pipelined, hipStream_t s);
 

@@ -8,9 +8,11 @@ namespace trt {
 
 // What the prep kernel leaves on the device for the others.
 struct XentHead {
-  int32_t live;    // tokens that take part
-  float c;         // largest weight s_t (backward)
-  float factor;    // c over G's scale
+  int32_t live;      // tokens that take part
+  float c;           // largest weight s_t (backward)
+  float factor;      // c over G's scale
+  int32_t slice;     // K of a slice of dX's product (backward)
+  int32_t slices;    // slices of a whole piece
 };
 
 // Largest number of tokens: one workgroup of 256 threads a token in a launch
@@ -25,6 +27,39 @@ constexpr int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * t
 // Tokens up to which the forward pass takes every row in place: they fit one
 // tile row of 128, so a list of live tokens would save no work.
 constexpr int64_t kXentInPlace = 128;
+
+#if defined(__HIPCC__)
+#define TRT_XENT_HD __host__ __device__
+#else
+#define TRT_XENT_HD
+#endif
+
+// dX has few tiles where live tokens or the width are few: its K is then cut
+// into slices, each with sums of its own.  The number that takes the least
+// time, counted in K: rounds of the compute units (two small tiles to one)
+// times a slice's K and what a tile costs beside its products (about 10 us,
+// of 23 us per 1024 of K); at least 512 of K each, and no more than four
+// rounds of 256 in all.
+TRT_XENT_HD constexpr int64_t xent_slices(int64_t rows, int64_t width, int64_t k, bool wide) {
+  const int64_t tile = wide ? 256 : 128, units = wide ? 256 : 512, beside = 450;
+  const int64_t tiles = ((rows + tile - 1) / tile) * ((width + tile - 1) / tile);
+  int64_t best = 1, least = 0;
+  for (int64_t s = 1; s <= 32 && (s == 1 || (s * 512 <= k && s * tiles <= 1024)); ++s) {
+    const int64_t cost = (tiles * s + units - 1) / units * (k / s + beside);
+    if (s == 1 || cost < least) {
+      best = s;
+      least = cost;
+    }
+  }
+  return best;
+}
+// K of a slice: a multiple of 64.
+TRT_XENT_HD constexpr int64_t xent_slice(int64_t rows, int64_t width, int64_t k, bool wide) {
+  const int64_t s = xent_slices(rows, width, k, wide);
+  return ((k + s - 1) / s + 63) / 64 * 64;
+}
+// Rows of a slice's sums: whole tiles.
+TRT_XENT_HD constexpr int64_t xent_sum_rows(int64_t rows) { return (rows + 255) / 256 * 256; }
 
 struct XentFwdPlan {
   bool wide;           // 256x256 tiles, else 128x128
@@ -57,7 +92,7 @@ struct XentBwdPlan {
   int64_t pieces;
   int64_t padded;      // width of X' and of the sums' rows, a multiple of 8
   bool wide_g, wide_x, wide_w;   // 256-wide tiles for G, dX and dW
-  int64_t slice, slices;         // of a piece's K in dX
+  int64_t most_tiles;            // workgroups of dX's product, for any number of live tokens
   int64_t head, list, place, weight, info, x, g, sums;   // byte offsets
   int64_t bytes;
 };
@@ -85,18 +120,21 @@ constexpr XentBwdPlan xent_bwd_plan(int64_t tokens, int64_t vocab, int64_t width
   p.padded = round_up(width, 8);
   p.wide_g = xent_wide(tokens, p.piece);
   p.wide_w = xent_wide(p.piece, width);
-  // dX has few tiles where tokens or width are small: its K is cut into
-  // slices of at least 512 until there are about two tiles for every compute
-  // unit (one of the 256-wide ones)
   p.wide_x = tokens > 192 && width > 192;
-  const int64_t tile = p.wide_x ? 256 : 128;
-  const int64_t tiles = ((tokens + tile - 1) / tile) * ((width + tile - 1) / tile);
-  const int64_t want = (p.wide_x ? 256 : 512) / tiles;
-  int64_t slices = want;
-  if (slices > p.piece / 512) slices = p.piece / 512;
-  if (slices < 1) slices = 1;
-  p.slice = round_up((p.piece + slices - 1) / slices, 64);
-  p.slices = (p.piece + p.slice - 1) / p.slice;
+  // the sums' room and the grid, for whatever number of tokens is live
+  const int64_t tile = p.wide_x ? 256 : 128, cols = (width + tile - 1) / tile;
+  const int64_t k = p.piece < vocab ? p.piece : vocab;
+  int64_t sum_rows = 0;
+  for (int64_t r = 0; r < tokens; r += tile) {
+    const int64_t rows = tokens - r < tile ? tokens : r + tile;
+    const int64_t s = xent_slices(rows, width, k, p.wide_x);
+    const int64_t tiles = ((rows + tile - 1) / tile) * cols;
+    if (s * xent_sum_rows(rows) > sum_rows) sum_rows = s * xent_sum_rows(rows);
+    if (s * tiles > p.most_tiles) p.most_tiles = s * tiles;
+    // from here on there is one slice and both grow with the rows alone: on to
+    // the last
+    if (tiles > 512 && rows < tokens) r = (tokens - 1) / tile * tile - tile;
+  }
   int64_t at = 0;
   auto take = [&](int64_t n) { const int64_t o = at; at += round_up(n, 256); return o; };
   p.head = take(sizeof(XentHead));
@@ -106,7 +144,7 @@ constexpr XentBwdPlan xent_bwd_plan(int64_t tokens, int64_t vocab, int64_t width
   p.info = take(tokens * 16);
   p.x = take(tokens * p.padded * 2);
   p.g = take(tokens * p.piece * 2);
-  p.sums = take(p.slices * tokens * p.padded * 4);
+  p.sums = take(sum_rows * p.padded * 4);
   p.bytes = at;
   return p;
 }

@@ -85,6 +85,11 @@ __global__ __launch_bounds__(kPrepThreads) void xent_prep_kernel(XentPrepArgs a)
     a.head->live = base;
     a.head->c = c;
     a.head->factor = c / a.scale;
+    if (a.dloss) {
+      const int64_t slice = xent_slice(base, a.width, a.k, a.wide != 0);
+      a.head->slice = (int32_t)slice;
+      a.head->slices = (int32_t)((a.k + slice - 1) / slice);
+    }
   }
 }
 
@@ -179,12 +184,14 @@ __global__ __launch_bounds__(256) void xent_input_finish_kernel(XentInputFinishA
   const int64_t t = blockIdx.x;
   const int m = a.place[t];
   const float w = m < 0 ? 0.f : a.weight[m];
+  const int slices = a.head->slices;
+  const int64_t stride = xent_sum_rows(a.head->live) * a.ld;
   for (int i = 4 * threadIdx.x; i < a.width; i += 1024) {
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
     if (m >= 0) {   // the sums' rows are padded to whole eights
       const float* p = a.sums + (int64_t)m * a.ld + i;
 #pragma unroll 8
-      for (int s = 0; s < a.slices; ++s) v += *reinterpret_cast<const f32x4*>(p + s * a.slice_stride);
+      for (int s = 0; s < slices; ++s) v += *reinterpret_cast<const f32x4*>(p + s * stride);
       v *= w;
     }
     const int64_t at = t * a.lddx + i;
