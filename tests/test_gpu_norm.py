@@ -15,7 +15,7 @@ and with w = dy gamma, U = rms(w) >= mean |w|, mean |w h|:
 
     |error of dx| <= half step + u r (200 U + 80 |w| + 260 U |h|)
 
-A parameter gradient adds rows / slices rows in a workgroup's running sum, 4
+A parameter gradient adds rows / slices rows in a workgroup's running sums, 16
 groups, slices / 16 slices in a wave and 16 waves: with `depth` their sum,
 
     |error of dgamma| <= half step + u (depth sum |dy h| + sum |dy| (64 + 72 |h|))
@@ -119,7 +119,7 @@ def run_case(rows, cols, dtype, pdtype, *, pad=0, offset=0, eps=1e-5, seed=0, me
     rms = np.sqrt((w * w).mean(1, keepdims=True))
     check(dx, rdx, half_step(rdx, dtype) + U * r * (200 * rms + 80 * w + 260 * rms * np.abs(h)), what + " dx")
     slices = need // (8 * cols)
-    depth = -(-rows // slices) + 4 + -(-slices // 16) + 16
+    depth = -(-rows // slices) + 16 + -(-slices // 16) + 16
     check(dgamma, rdg, half_step(rdg, pdtype) + U * (depth * np.abs(hdy * h).sum(0) +
                                                      (np.abs(hdy) * (64 + 72 * np.abs(h))).sum(0)), what + " dgamma")
     check(dbeta, rdb, half_step(rdb, pdtype) + U * depth * np.abs(hdy).sum(0), what + " dbeta")

@@ -8,22 +8,22 @@ namespace trt {
 
 namespace {
 
-// Waves per row W and 16-byte chunks per lane K for a row of `chunks` chunks,
-// the same for both directions.  A row of up to 128 chunks (1024 16-bit
-// elements) is one wave's: no barrier, four rows to a workgroup.  Longer rows
-// take 4, 8 and 16 waves, so that a lane holds no more than 2 chunks up to
-// 2048 of them and 4 beyond: the backward pass keeps two running sums per
-// element of them in registers.
+// Waves per row W and 16-byte chunks per lane K for a row of `chunks` chunks.
+// A row of up to 128 chunks (1024 16-bit elements) is one wave's: no barrier,
+// several rows to a workgroup.  Longer rows take 4, 8 and 16 waves, so that a
+// lane holds few chunks: the backward pass keeps two running sums per element
+// of them in registers.
 struct Shape {
   int w, k;
 };
-constexpr Shape shape_of(int64_t chunks) {
+constexpr Shape shape_of(int64_t chunks, bool backward) {
   if (chunks <= 64) return {1, 1};
   if (chunks <= 128) return {1, 2};
   if (chunks <= 256) return {4, 1};
   if (chunks <= 512) return {4, 2};
+  if (chunks <= 768 && !backward) return {4, 3};
   if (chunks <= 1024) return {8, 2};
-  if (chunks <= 2048) return {16, 2};
+  if (chunks <= 2048) return backward ? Shape{8, 4} : Shape{16, 2};
   return {16, 4};
 }
 static_assert(kNormMaxRowBytes / 16 == 16 * 64 * 4, "the longest row is one workgroup's");
@@ -36,19 +36,41 @@ int grid_of(int64_t rows, int groups, int most) {
   return (int)((need + turns - 1) / turns);
 }
 
+// Forward workgroups to a compute unit, 16 waves in all (measured on 16384
+// rows of 8192 16-bit elements: 94 us, against 107 with twice as many), but
+// for one-wave rows, whose short loads want 32 (65536 rows of 512: 25.7 us
+// against 28.5).  Backward: one of 16 waves.
 template <int W>
-constexpr int forward_most() { return W <= 4 ? 8 : (W == 8 ? 4 : 2); }
-template <int W>
-constexpr int backward_most() { return W <= 4 ? 2 : 1; }
+constexpr int forward_most() { return W == 1 ? 8 : 16 / W; }
 
-template <int DT, class F>
+template <int DT, bool BACKWARD, class F>
 auto with_shape(int64_t cols, F&& f) {
-  const Shape s = shape_of((cols + RowChunk<DT>::VEC - 1) / RowChunk<DT>::VEC);
+  const Shape s = shape_of((cols + RowChunk<DT>::VEC - 1) / RowChunk<DT>::VEC, BACKWARD);
   if (s.w == 1) return s.k == 1 ? f.template operator()<1, 1>() : f.template operator()<1, 2>();
-  if (s.w == 4) return s.k == 1 ? f.template operator()<4, 1>() : f.template operator()<4, 2>();
-  if (s.w == 8) return f.template operator()<8, 2>();
-  return s.k == 2 ? f.template operator()<16, 2>() : f.template operator()<16, 4>();
+  if (s.w == 4) {
+    if constexpr (!BACKWARD)
+      if (s.k == 3) return f.template operator()<4, 3>();
+    return s.k == 1 ? f.template operator()<4, 1>() : f.template operator()<4, 2>();
+  }
+  if constexpr (BACKWARD) {
+    if (s.w == 8) return s.k == 2 ? f.template operator()<8, 2>() : f.template operator()<8, 4>();
+  } else {
+    if (s.w == 8) return f.template operator()<8, 2>();
+    if (s.k == 2) return f.template operator()<16, 2>();
+  }
+  return f.template operator()<16, 4>();
 }
+
+// Waves of a backward workgroup: 16, rows of which the registers allow it and
+// where such workgroups fill the 256 units; else as the forward pass has them.
+template <int W, int K>
+constexpr int kBwdWaves = W == 8 && K == 4 ? 8 : 16;
+template <int W, int K>
+bool bwd_large(int64_t rows) {
+  return (rows + kBwdWaves<W, K> / W - 1) / (kBwdWaves<W, K> / W) >= 256;
+}
+template <int W>
+constexpr int kBwdFewWaves = W == 1 ? 4 : W;
 
 template <class F>
 hipError_t with_types(int dt, int pdt, F&& f) {
@@ -60,8 +82,8 @@ hipError_t with_types(int dt, int pdt, F&& f) {
 
 template <int DT>
 int slices_of(int64_t rows, int64_t cols) {
-  return with_shape<DT>(cols, [&]<int W, int K>() {
-    return grid_of(rows, NormShape<W>::GROUPS, backward_most<W>());
+  return with_shape<DT, true>(cols, [&]<int W, int K>() {
+    return grid_of(rows, (bwd_large<W, K>(rows) ? kBwdWaves<W, K> : kBwdFewWaves<W>) / W, 1);
   });
 }
 
@@ -73,7 +95,7 @@ int norm_slices(int64_t rows, int64_t cols, int dt) {
 
 hipError_t launch_layernorm(const NormArgs& a, int dt, int pdt, hipStream_t s) {
   return with_types(dt, pdt, [&]<int DT, int PDT>() {
-    return with_shape<DT>(a.cols, [&]<int W, int K>() {
+    return with_shape<DT, false>(a.cols, [&]<int W, int K>() {
       const int wgs = grid_of(a.rows, NormShape<W>::GROUPS, forward_most<W>());
       return launch(layernorm_kernel<DT, PDT, W, K>, dim3(wgs), dim3(NormShape<W>::THREADS), 0, s, a);
     });
@@ -84,8 +106,11 @@ hipError_t launch_layernorm_bwd(const NormArgs& a, void* dgamma, void* dbeta, in
                                 hipStream_t s) {
   const int slices = norm_slices(a.rows, a.cols, dt);
   return with_types(dt, pdt, [&]<int DT, int PDT>() {
-    const hipError_t e = with_shape<DT>(a.cols, [&]<int W, int K>() {
-      return launch(layernorm_bwd_kernel<DT, PDT, W, K>, dim3(slices), dim3(NormShape<W>::THREADS), 0, s, a);
+    const hipError_t e = with_shape<DT, true>(a.cols, [&]<int W, int K>() {
+      constexpr int MANY = kBwdWaves<W, K>, FEW = kBwdFewWaves<W>;
+      if (bwd_large<W, K>(a.rows))
+        return launch(layernorm_bwd_kernel<DT, PDT, W, K, MANY>, dim3(slices), dim3(64 * MANY), 0, s, a);
+      return launch(layernorm_bwd_kernel<DT, PDT, W, K, FEW>, dim3(slices), dim3(64 * FEW), 0, s, a);
     });
     if (e != hipSuccess || !a.part) return e;
     const NormParamsArgs q{a.part, dgamma, dbeta, slices, a.cols};

@@ -1,11 +1,25 @@
 // kern_xent.hip -- the cross entropy's small kernels.
 #include "launch.hpp"
 #include "xent_rows.hpp"
+#include "xent_stream.hpp"
 
 namespace trt {
 
 hipError_t launch_xent_prep(const XentPrepArgs& a, hipStream_t s) {
-  return launch(xent_prep_kernel, dim3(1), dim3(kPrepThreads), 0, s, a);
+  if (a.dloss) return launch(xent_prep_kernel<true>, dim3(1), dim3(kPrepThreads), 0, s, a);
+  return launch(xent_prep_kernel<false>, dim3(1), dim3(kPrepThreads), 0, s, a);
+}
+
+hipError_t launch_xent_stream(const XentStatsArgs& a, int dt, hipStream_t s) {
+  const dim3 grid((a.N + kXentStreamTile - 1) / kXentStreamTile);
+  auto run = [&]<int T>() {
+    const dim3 block(kXentStreamThreads);
+    if (dt == DT_F16) return launch(xent_stream_kernel<DT_F16, T>, grid, block, 0, s, a);
+    return launch(xent_stream_kernel<DT_BF16, T>, grid, block, 0, s, a);
+  };
+  if (a.M == 1) return run.template operator()<1>();
+  if (a.M == 2) return run.template operator()<2>();
+  return run.template operator()<4>();
 }
 
 // Rows to a workgroup: 64, so that a wave reads whole lines of a tile's

@@ -99,24 +99,26 @@ __device__ __forceinline__ float wave_sum(float v) {
 }
 
 // Sums of N values over the W waves of a row.  W > 1: the waves meet in LDS,
-// in `buf` (two turns used alternately, so one barrier a turn suffices: a
-// wave writes a turn's slots again only after the next turn's barrier, which
-// every wave reaches with its reads of the first turn done).
+// in the slots of `buf` from `first` on (two turns used alternately, so one
+// barrier a turn suffices: a wave writes a turn's slots again only after the
+// next turn's barrier, which every wave reaches with its reads of the first
+// turn done).  Every wave of the workgroup calls it.
 template <int W, int N>
-__device__ __forceinline__ void row_sums(float (&v)[N], float (*buf)[16][4], int& turn, int wave) {
+__device__ __forceinline__ void row_sums(float (&v)[N], float (*buf)[16][4], int& turn, int wave,
+                                         int first) {
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
   if constexpr (W > 1) {
     static_assert(W <= 16 && N <= 4, "one slot per wave and value");
     if ((threadIdx.x & 63) == 0)
 #pragma unroll
-      for (int i = 0; i < N; ++i) buf[turn][wave][i] = v[i];
+      for (int i = 0; i < N; ++i) buf[turn][first + wave][i] = v[i];
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      float s = buf[turn][0][i];
+      float s = buf[turn][first][i];
 #pragma unroll
-      for (int w = 1; w < W; ++w) s += buf[turn][w][i];
+      for (int w = 1; w < W; ++w) s += buf[turn][first + w][i];
       v[i] = s;
     }
     turn ^= 1;
@@ -136,7 +138,7 @@ template <int DT, int PDT, int W, int K>
 __global__ __launch_bounds__(NormShape<W>::THREADS) void layernorm_kernel(NormArgs a) {
   using C = RowChunk<DT>;
   constexpr int VEC = C::VEC, LANES = 64 * W, GROUPS = NormShape<W>::GROUPS;
-  constexpr bool KEEP = K <= 2;
+  constexpr bool KEEP = K <= 3;
   __shared__ float buf[2][16][4];
   // the wave's index in a scalar register: row addresses are then scalar too
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -175,7 +177,7 @@ __global__ __launch_bounds__(NormShape<W>::THREADS) void layernorm_kernel(NormAr
     for (int k = 0; k < K; ++k)
 #pragma unroll
       for (int e = 0; e < VEC; ++e) s[0] += C::elem(x[k], e);
-    row_sums<W, 1>(s, buf, turn, wave);
+    row_sums<W, 1>(s, buf, turn, wave, W * grp);
     keep_packed(x);
     const float m = rounded(s[0] * inv);
     float q[2] = {0.f, 0.f};
@@ -186,7 +188,7 @@ __global__ __launch_bounds__(NormShape<W>::THREADS) void layernorm_kernel(NormAr
         q[0] += d;
         q[1] += d * d;
       });
-    row_sums<W, 2>(q, buf, turn, wave);
+    row_sums<W, 2>(q, buf, turn, wave, W * grp);
     keep_packed(x);
     const float dbar = q[0] * inv;
     const float rstd = 1.f / sqrtf(fmaxf(q[1] * inv - dbar * dbar, 0.f) + a.eps);
@@ -211,14 +213,19 @@ __global__ __launch_bounds__(NormShape<W>::THREADS) void layernorm_kernel(NormAr
 // them to its slice of `part` at the end, and norm_params_kernel adds the
 // slices in order.  The grid is fixed by the sizes (norm_grid), so the sums'
 // order is too: the results repeat bit for bit.
-// AHEAD: the next row is loaded ahead and gamma kept in registers.  Rows of
-// 16 waves leave no registers for that (1024 threads share them): their other
-// waves cover the latency instead.
-template <int DT, int PDT, int W, int K>
-__global__ __launch_bounds__(NormShape<W>::THREADS) void layernorm_bwd_kernel(NormArgs a) {
+// A workgroup is 16 waves, 16 / W rows at a time, and there is one to a
+// compute unit: the fewer slices, the fewer bytes beside the rows' own (with
+// workgroups of one row, two to a unit, the slices were 8 % of the traffic of
+// 16384 rows of 8192, and 8 % of the time).
+// AHEAD: the next row is loaded ahead and gamma kept in registers; rows of 16
+// waves leave none for that.
+// (Too few rows to give every unit one of 16 waves take the forward pass's
+// smaller ones.)
+template <int DT, int PDT, int W, int K, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void layernorm_bwd_kernel(NormArgs a) {
   using C = RowChunk<DT>;
-  constexpr int VEC = C::VEC, LANES = 64 * W, GROUPS = NormShape<W>::GROUPS;
-  constexpr bool AHEAD = W < 16;
+  constexpr int VEC = C::VEC, LANES = 64 * W, GROUPS = WAVES / W;
+  constexpr bool AHEAD = K <= 2 && W < 16;
   __shared__ float buf[2][16][4];
   __shared__ float fold[GROUPS > 1 ? GROUPS : 1][GROUPS > 1 ? LANES * VEC * K : 1];
   // the wave's index in a scalar register: row addresses are then scalar too
@@ -241,6 +248,8 @@ __global__ __launch_bounds__(NormShape<W>::THREADS) void layernorm_bwd_kernel(No
   u32x4 nx[AHEAD ? K : 1], ny[AHEAD ? K : 1];
   float kept[AHEAD ? K : 1][VEC];
   if constexpr (AHEAD) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) nx[k] = ny[k] = u32x4{0u, 0u, 0u, 0u};
     if (r < a.rows) {
       load(nx, a.x, a.ldx, r);
       load(ny, a.dy, a.lddy, r);
@@ -254,7 +263,10 @@ __global__ __launch_bounds__(NormShape<W>::THREADS) void layernorm_bwd_kernel(No
 #pragma unroll
     for (int e = 0; e < VEC; ++e) dg[k][e] = db[k][e] = 0.f;
 
-  for (; r < a.rows; r += step) {
+  // every wave takes as many turns as the workgroup's first row needs; one
+  // past the last row works on zeros and keeps nothing
+  for (int64_t r0 = (int64_t)blockIdx.x * GROUPS; r0 < a.rows; r0 += step, r += step) {
+    const bool live = r < a.rows;
     u32x4 x[K], y[K];
     if constexpr (AHEAD) {
 #pragma unroll
@@ -264,15 +276,19 @@ __global__ __launch_bounds__(NormShape<W>::THREADS) void layernorm_bwd_kernel(No
         load(ny, a.dy, a.lddy, r + step);
       }
     } else {
-      load(x, a.x, a.ldx, r);
-      load(y, a.dy, a.lddy, r);
+#pragma unroll
+      for (int k = 0; k < K; ++k) x[k] = y[k] = u32x4{0u, 0u, 0u, 0u};
+      if (live) {
+        load(x, a.x, a.ldx, r);
+        load(y, a.dy, a.lddy, r);
+      }
     }
     float s[1] = {0.f};
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
       for (int e = 0; e < VEC; ++e) s[0] += C::elem(x[k], e);
-    row_sums<W, 1>(s, buf, turn, wave);
+    row_sums<W, 1>(s, buf, turn, wave, W * grp);
     keep_packed(x);
     const float m = rounded(s[0] * inv);
     auto gamma_of = [&](int k, float (&g)[VEC]) {
@@ -297,13 +313,14 @@ __global__ __launch_bounds__(NormShape<W>::THREADS) void layernorm_bwd_kernel(No
         q[3] += u * d;
       });
     }
-    row_sums<W, 4>(q, buf, turn, wave);
+    row_sums<W, 4>(q, buf, turn, wave, W * grp);
     keep_packed(x);
     keep_packed(y);
     const float dbar = q[0] * inv;
     const float rstd = 1.f / sqrtf(fmaxf(q[1] * inv - dbar * dbar, 0.f) + a.eps);
     const float c1 = q[2] * inv;
     const float c2 = rstd * (q[3] * inv - dbar * c1);   // mean(u h)
+    if (!live) continue;
     char* p = static_cast<char*>(a.out) + r * a.ldo * (int64_t)sizeof(typename C::Elem);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -333,7 +350,7 @@ __global__ __launch_bounds__(NormShape<W>::THREADS) void layernorm_bwd_kernel(No
 #pragma unroll
         for (int e = 0; e < VEC; ++e) fold[grp][VEC * (me + k * LANES) + e] = acc[k][e];
       __syncthreads();
-      for (int c = threadIdx.x; c < n; c += NormShape<W>::THREADS) {
+      for (int c = threadIdx.x; c < n; c += 64 * WAVES) {
         float t = fold[0][c];
 #pragma unroll
         for (int q = 1; q < GROUPS; ++q) t += fold[q][c];

@@ -96,13 +96,14 @@ trt_status trt_linear_xent(int64_t tokens, int64_t vocab, int64_t width, const v
     if (e != hipSuccess) return trt::launched(e, "cross entropy launch");
   }
 
-  // one launch per 2 GiB of w
+  // one launch per 2 GiB of w (the stream over W addresses it whole)
   trt::XentStatsArgs a{};
   const bool vec = width % 8 == 0 && ldx % 8 == 0 && ldw % 8 == 0 && aligned16(x) && aligned16(w);
+  const bool stream_w = vec && tokens <= trt::kXentStreamTokens;
   const int64_t chunk = kExtent / (2 * ldw) / 256 * 256;
   const bool pipelined = vec && chunk >= 256 && ((tokens - 1) * ldx + width) * 2 < kExtent;
-  const int64_t step = pipelined ? chunk : vocab;
-  const int64_t tile = pipelined && plan.wide ? 256 : 128;
+  const int64_t step = pipelined && !stream_w ? chunk : vocab;
+  const int64_t tile = stream_w ? trt::kXentStreamTile : pipelined && plan.wide ? 256 : 128;
   for (int64_t v0 = 0; v0 < vocab; v0 += step) {
     const int64_t n = vocab - v0 < step ? vocab - v0 : step;
     a.A = static_cast<const uint16_t*>(x);
@@ -123,7 +124,8 @@ trt_status trt_linear_xent(int64_t tokens, int64_t vocab, int64_t width, const v
     a.ldp = tokens;
     a.tile0 = (int32_t)(v0 / tile);
     a.col0 = v0;
-    e = trt::launch_xent_stats(a, dtype, plan.wide, pipelined, st);
+    e = stream_w ? trt::launch_xent_stream(a, dtype, st)
+                 : trt::launch_xent_stats(a, dtype, plan.wide, pipelined, st);
     if (e != hipSuccess) return trt::launched(e, "cross entropy launch");
   }
   trt::XentCombineArgs c{};

@@ -106,6 +106,8 @@ struct XentInputFinishArgs {
 // pipelined: the operands allow 16-byte copies; otherwise the generic kernel
 // on 128x128 tiles runs the same epilogue.
 hipError_t launch_xent_stats(XentStatsArgs a, int dt, bool wide, bool pipelined, hipStream_t s);
+// For up to kXentStreamTokens tokens in place, where the copies' conditions hold.
+hipError_t launch_xent_stream(const XentStatsArgs& a, int dt, hipStream_t s);
 hipError_t launch_xent_grad(XentGradArgs a, int dt, bool wide, bool pipelined, hipStream_t s);
 hipError_t launch_xent_input(XentInputArgs a, int dt, bool wide, bool pipelined, int64_t groups,
                              hipStream_t s);

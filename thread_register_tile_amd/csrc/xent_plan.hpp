@@ -40,26 +40,33 @@ constexpr int64_t kXentInPlace = 128;
 // times a slice's K and what a tile costs beside its products (about 10 us,
 // of 23 us per 1024 of K); at least 512 of K each, and no more than four
 // rounds of 256 in all.
-TRT_XENT_HD constexpr int64_t xent_slices(int64_t rows, int64_t width, int64_t k, bool wide) {
-  const int64_t tile = wide ? 256 : 128, units = wide ? 256 : 512, beside = 450;
-  const int64_t tiles = ((rows + tile - 1) / tile) * ((width + tile - 1) / tile);
-  int64_t best = 1, least = 0;
-  for (int64_t s = 1; s <= 32 && (s == 1 || (s * 512 <= k && s * tiles <= 1024)); ++s) {
-    const int64_t cost = (tiles * s + units - 1) / units * (k / s + beside);
-    if (s == 1 || cost < least) {
-      best = s;
-      least = cost;
-    }
-  }
+constexpr int kXentMostSlices = 32;
+// Time of s slices, or the largest value where so many are not allowed.
+TRT_XENT_HD constexpr uint64_t xent_slice_cost(uint32_t s, uint32_t tiles, uint32_t k, bool wide) {
+  const uint32_t units = wide ? 256 : 512, beside = 450;
+  if (s > 1 && (s * 512 > k || (uint64_t)s * tiles > 1024)) return ~uint64_t(0);
+  return (uint64_t)((tiles * s + units - 1) / units) * (k / s + beside);
+}
+TRT_XENT_HD constexpr uint32_t xent_input_tiles(int64_t rows, int64_t width, bool wide) {
+  const uint32_t tile = wide ? 256 : 128;
+  return (((uint32_t)rows + tile - 1) / tile) * (((uint32_t)width + tile - 1) / tile);
+}
+// The number of slices (the least of equal ones).
+constexpr int64_t xent_slices(int64_t rows, int64_t width, int64_t k, bool wide) {
+  const uint32_t tiles = xent_input_tiles(rows, width, wide);
+  uint32_t best = 1;
+  for (uint32_t s = 2; s <= kXentMostSlices; ++s)
+    if (xent_slice_cost(s, tiles, (uint32_t)k, wide) < xent_slice_cost(best, tiles, (uint32_t)k, wide)) best = s;
   return best;
 }
-// K of a slice: a multiple of 64.
-TRT_XENT_HD constexpr int64_t xent_slice(int64_t rows, int64_t width, int64_t k, bool wide) {
-  const int64_t s = xent_slices(rows, width, k, wide);
-  return ((k + s - 1) / s + 63) / 64 * 64;
-}
+// K of each of s slices: a multiple of 64.
+TRT_XENT_HD constexpr uint32_t xent_slice(uint32_t s, uint32_t k) { return ((k + s - 1) / s + 63) / 64 * 64; }
 // Rows of a slice's sums: whole tiles.
 TRT_XENT_HD constexpr int64_t xent_sum_rows(int64_t rows) { return (rows + 255) / 256 * 256; }
+
+// Tokens up to which the forward pass streams W, 64 entries to a workgroup.
+constexpr int64_t kXentStreamTokens = 4;
+constexpr int kXentStreamTile = 64;
 
 struct XentFwdPlan {
   bool wide;           // 256x256 tiles, else 128x128
@@ -79,7 +86,9 @@ constexpr XentFwdPlan xent_fwd_plan(int64_t tokens, int64_t vocab) {
   int64_t at = 0;
   auto take = [&](int64_t n) { const int64_t o = at; at += round_up(n, 256); return o; };
   p.head = take(sizeof(XentHead));
-  p.part = take((vocab + 127) / 128 * tokens * 8);   // for either tile
+  // for the smallest tile that any kernel of so many tokens takes
+  const int64_t tile = tokens <= kXentStreamTokens ? kXentStreamTile : 128;
+  p.part = take((vocab + tile - 1) / tile * tokens * 8);
   p.at = take(tokens * 4);
   p.list = take(tokens > kXentInPlace ? tokens * 4 : 0);
   p.want = take(tokens > kXentInPlace ? tokens * 4 : 0);
@@ -119,7 +128,9 @@ constexpr XentBwdPlan xent_bwd_plan(int64_t tokens, int64_t vocab, int64_t width
   p.pieces = (vocab + p.piece - 1) / p.piece;
   p.padded = round_up(width, 8);
   p.wide_g = xent_wide(tokens, p.piece);
-  p.wide_w = xent_wide(p.piece, width);
+  // dW of few tokens is all store: twice the workgroups to a unit (16 tokens:
+  // 185 us against 168, 512: 417 against 401, 1024: 681 against 690, 32000 x 4096)
+  p.wide_w = tokens > 768 && xent_wide(p.piece, width);
   p.wide_x = tokens > 192 && width > 192;
   // the sums' room and the grid, for whatever number of tokens is live
   const int64_t tile = p.wide_x ? 256 : 128, cols = (width + tile - 1) / tile;

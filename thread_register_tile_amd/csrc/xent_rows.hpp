@@ -21,6 +21,9 @@ __device__ __forceinline__ float xent_weight(const XentPrepArgs& a, int64_t t, f
   return __builtin_fmaxf(__builtin_fabsf(dl), __builtin_fabsf(both));
 }
 
+// (BACKWARD as a template argument, so that the loads of a thread's tokens are
+// all issued before the first of them is used.)
+template <bool BACKWARD>
 __global__ __launch_bounds__(kPrepThreads) void xent_prep_kernel(XentPrepArgs a) {
   __shared__ int count[16];
   __shared__ float top[16];
@@ -29,18 +32,22 @@ __global__ __launch_bounds__(kPrepThreads) void xent_prep_kernel(XentPrepArgs a)
   float c = 0.f;
   for (int64_t t0 = 0; t0 < a.tokens; t0 += kPrepThreads * kPrepEach) {
     const int64_t first = t0 + (int64_t)t * kPrepEach;
+    int64_t target[kPrepEach];
+    float s[kPrepEach];
+#pragma unroll
+    for (int e = 0; e < kPrepEach; ++e) {
+      const int64_t tok = first + e < a.tokens ? first + e : a.tokens - 1;
+      target[e] = a.target[tok];
+      float dl, both;
+      s[e] = BACKWARD ? xent_weight(a, tok, dl, both) : 1.f;
+    }
     uint32_t keep = 0;
 #pragma unroll
-    for (int e = 0; e < kPrepEach; ++e)
-      if (first + e < a.tokens && a.target[first + e] != a.ignore) {
-        float s = 1.f;
-        if (a.dloss) {
-          float dl, both;
-          s = xent_weight(a, first + e, dl, both);
-          c = __builtin_fmaxf(c, s);
-        }
-        if (s != 0.f) keep |= 1u << e;
-      }
+    for (int e = 0; e < kPrepEach; ++e) {
+      const bool live = first + e < a.tokens && target[e] != a.ignore && s[e] != 0.f;
+      keep |= live ? 1u << e : 0u;
+      c = live ? __builtin_fmaxf(c, s[e]) : c;
+    }
     int upto = __popc(keep);   // inclusive count over the wave's lanes
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
@@ -61,14 +68,11 @@ __global__ __launch_bounds__(kPrepThreads) void xent_prep_kernel(XentPrepArgs a)
       const int64_t tok = first + e;
       if (tok >= a.tokens) break;
       const bool live = (keep >> e) & 1u;
-      if (a.place) a.place[tok] = live ? at : -1;
+      if (BACKWARD) a.place[tok] = live ? at : -1;
       if (live) {
-        if (a.want) {
-          const int64_t v = a.target[tok];
-          a.want[at] = v >= 0 && v < a.vocab ? (int32_t)v : -1;
-        }
+        if (!BACKWARD) a.want[at] = target[e] >= 0 && target[e] < a.vocab ? (int32_t)target[e] : -1;
         a.list[at++] = (int32_t)tok;
-      } else if (a.loss) {
+      } else if (!BACKWARD) {
         a.loss[tok] = 0.f;
         a.lse[tok] = 0.f;
       }
@@ -76,25 +80,37 @@ __global__ __launch_bounds__(kPrepThreads) void xent_prep_kernel(XentPrepArgs a)
     base += all;
     __syncthreads();
   }
+  if (BACKWARD) {
 #pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) c = __builtin_fmaxf(c, __shfl_xor(c, off));
-  if (lane == 0) top[wave] = c;
-  __syncthreads();
-  if (t == 0) {
-    for (int w = 1; w < 16; ++w) c = __builtin_fmaxf(c, top[w]);
-    a.head->live = base;
-    a.head->c = c;
-    a.head->factor = c / a.scale;
-    if (a.dloss) {
-      const int64_t slice = xent_slice(base, a.width, a.k, a.wide != 0);
-      a.head->slice = (int32_t)slice;
-      a.head->slices = (int32_t)((a.k + slice - 1) / slice);
+    for (int off = 32; off >= 1; off >>= 1) c = __builtin_fmaxf(c, __shfl_xor(c, off));
+    if (lane == 0) top[wave] = c;
+    __syncthreads();
+    if (wave == 0) {
+      c = top[lane & 15];
+#pragma unroll
+      for (int off = 8; off >= 1; off >>= 1) c = __builtin_fmaxf(c, __shfl_xor(c, off));
+      // the number of slices of dX's product: lane s - 1 weighs s of them, the
+      // least cost and of those the least number is taken
+      const uint32_t tiles = xent_input_tiles(base, a.width, a.wide != 0);
+      const uint32_t mine = lane < kXentMostSlices ? lane + 1 : 1;
+      uint64_t cost = xent_slice_cost(mine, tiles, a.k, a.wide != 0);
+      uint32_t best = mine;
+#pragma unroll
+      for (int off = 32; off >= 1; off >>= 1) {
+        const uint64_t other = __shfl_xor(cost, off);
+        const uint32_t its = __shfl_xor(best, off);
+        if (other < cost || (other == cost && its < best)) cost = other, best = its;
+      }
+      if (lane == 0) {
+        const uint32_t slice = xent_slice(best, a.k);
+        *a.head = XentHead{base, c, c / a.scale, (int32_t)slice, (int32_t)((a.k + slice - 1) / slice)};
+      }
     }
+  } else if (t == 0) {
+    a.head->live = base;
   }
 }
 
-// Joins a row's pairs: a workgroup of 256 threads takes R rows, 256 / R
-// threads to a row, thread j of them the tiles j, j + 256 / R, ...
 template <int R>
 __global__ __launch_bounds__(256) void xent_combine_kernel(XentCombineArgs a) {
   constexpr int EACH = 256 / R;
