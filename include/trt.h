@@ -563,7 +563,8 @@ trt_status trt_layernorm_bwd(int64_t rows, int64_t cols, const void* dy, int64_t
  * whose dloss and dlse are both zero.  A target outside [0, vocab) that
  * is not ignore_index gives loss = NaN (lse is the true one) and, in the
  * backward pass, a row of NaN in dx and NaN in dw: it is not read out of range.
- * A NaN or infinity among a live token's logits makes its loss NaN.
+ * A NaN or a positive infinity among a live token's logits makes its loss
+ * NaN; a logit of -infinity has probability zero.
  *
  * x, w: dtype (in_dtype) TRT_F16 or TRT_BF16, ldx, ldw >= width; target:
  * [tokens] int64; loss, lse: [tokens] binary32.  dx: [tokens, width], dw:
@@ -573,10 +574,10 @@ trt_status trt_layernorm_bwd(int64_t rows, int64_t cols, const void* dy, int64_t
  * the forward pass's.  Logits, statistics and all sums are binary32.  The
  * backward pass works through the vocabulary in pieces of `piece` entries
  * (0: the library's choice; else a multiple of 64 up to 2^20, TRT_ERR_ARG
- * otherwise) and rounds g, with the tokens' weights max(|dloss|, |dloss +
- * dlse|) taken out, once to in_dtype; with weights that differ between
- * tokens it rounds X times their ratio to the largest as well.  In binary16
- * that loses bits for tokens whose weight is below 2^-14 of the largest.
+ * otherwise) and rounds g over the largest of the tokens' weights max(|dloss|,
+ * |dloss + dlse|) once to in_dtype (for up to 64 tokens it keeps what that rounding leaves
+ * in a second number).  In binary16 that loses bits of a g below 2^-28 of
+ * that weight.
  * Results repeat bit for bit.
  *
  * workspace: device memory of at least trt_linear_xent_workspace_size(tokens,

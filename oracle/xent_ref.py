@@ -19,10 +19,15 @@ def forward(x, w, target, ignore=-100):
     loss, lse = np.zeros(len(target)), np.zeros(len(target))
     m = z.max(1, keepdims=True)
     lse[live] = (m + np.log(np.exp(z - m).sum(1, keepdims=True)))[:, 0]
-    # log of the sum of exp(z - z_target): no cancellation of two large numbers
-    rel = z - z[np.arange(len(z)), target[live]][:, None]
-    top = rel.max(1, keepdims=True)
-    loss[live] = (top + np.log(np.exp(rel - top).sum(1, keepdims=True)))[:, 0]
+    # log(1 + the others' exp(z - z_target)): no cancellation of two large
+    # numbers, and no loss of a small one against 1
+    at = target[live]
+    rel = z - z[np.arange(len(z)), at][:, None]
+    rel[np.arange(len(z)), at] = -np.inf
+    top = np.maximum(rel.max(1, keepdims=True), -1e300)
+    with np.errstate(divide="ignore"):
+        others = (top + np.log(np.exp(rel - top).sum(1, keepdims=True)))[:, 0]
+    loss[live] = np.logaddexp(0.0, others)
     return loss, lse
 
 

@@ -73,9 +73,11 @@ def test_workspace_sizes():
     # the pairs: 8 bytes for a token and 128 entries, nothing like the logits
     n = trt.linear_xent_workspace_size(8192, 131072, 4096)
     assert 8192 * 1024 * 8 <= n < 8192 * 1024 * 8 + (1 << 20)
-    # one piece of G, X and dX's sums
+    # one piece of G, X, and dX's sums, of which there are no more than 1024
+    # tiles of 256x256
     small = trt.linear_xent_bwd_workspace_size(8192, 131072, 4096, 8192)
-    assert 8192 * 8192 * 2 + 8192 * 4096 * 6 <= small < 8192 * 8192 * 2 + 8192 * 4096 * 6 + (1 << 20)
+    base = 8192 * 8192 * 2 + 8192 * 4096 * 2
+    assert base + 8192 * 4096 * 4 <= small < base + 1024 * 65536 * 4 + (1 << 20)
     assert trt.linear_xent_bwd_workspace_size(8192, 131072, 4096) > small
     # a piece beyond the vocabulary is the vocabulary
     assert trt.linear_xent_bwd_workspace_size(10, 100, 8, 128) == trt.linear_xent_bwd_workspace_size(10, 100, 8, 1 << 20)

@@ -41,7 +41,10 @@ hipError_t launch_xent_rows(const XentRowsArgs& a, int dt, hipStream_t s) {
 
 hipError_t launch_xent_input_finish(const XentInputFinishArgs& a, int64_t tokens, int odt,
                                     hipStream_t s) {
-  const dim3 grid((unsigned)tokens), block(256);
+  // few tokens have many slices to add: a wave for 256 columns, so that their
+  // reads spread over the units
+  const bool few = tokens <= 512;
+  const dim3 grid((unsigned)tokens, few ? (a.width + 255) / 256 : 1), block(few ? 64 : 256);
   if (odt == DT_F16) return launch(xent_input_finish_kernel<DT_F16>, grid, block, 0, s, a);
   if (odt == DT_BF16) return launch(xent_input_finish_kernel<DT_BF16>, grid, block, 0, s, a);
   return launch(xent_input_finish_kernel<DT_F32>, grid, block, 0, s, a);

@@ -188,7 +188,6 @@ trt_status trt_linear_xent_bwd(int64_t tokens, int64_t vocab, int64_t width, con
   auto* head = reinterpret_cast<trt::XentHead*>(ws + plan.head);
   auto* list = reinterpret_cast<int32_t*>(ws + plan.list);
   auto* place = reinterpret_cast<int32_t*>(ws + plan.place);
-  auto* weight = reinterpret_cast<float*>(ws + plan.weight);
   auto* info = reinterpret_cast<trt::XentRow*>(ws + plan.info);
   auto* xs = reinterpret_cast<uint16_t*>(ws + plan.x);
   auto* g = reinterpret_cast<uint16_t*>(ws + plan.g);
@@ -214,7 +213,7 @@ trt_status trt_linear_xent_bwd(int64_t tokens, int64_t vocab, int64_t width, con
   r.out = xs;
   r.lse = lse;
   r.info = info;
-  r.weight = weight;
+  r.prep.halves = plan.halves;
   r.ldx = ldx;
   r.ld = plan.padded;
   r.width = (int32_t)width;
@@ -222,7 +221,7 @@ trt_status trt_linear_xent_bwd(int64_t tokens, int64_t vocab, int64_t width, con
   if (const hipError_t e = trt::launch_xent_prep(r.prep, st); e != hipSuccess) return done(e);
   if (const hipError_t e = trt::launch_xent_rows(r, in_dtype, st); e != hipSuccess) return done(e);
 
-  const int64_t rows256 = trt::round_up(tokens, 256);
+  const int64_t rows256 = trt::round_up(tokens << (plan.halves ? 1 : 0), 256);   // of G and X'
   const bool vec_x = width % 8 == 0 && ldx % 8 == 0 && aligned16(x) &&
                      ((tokens - 1) * ldx + width) * 2 < kExtent;
   const bool vec_w = width % 8 == 0 && ldw % 8 == 0 && aligned16(w) &&
@@ -251,6 +250,7 @@ trt_status trt_linear_xent_bwd(int64_t tokens, int64_t vocab, int64_t width, con
     a.list = list;
     a.info = info;
     a.cols = (int32_t)n;
+    a.halves = plan.halves;
     a.col0 = v0;
     // the generic kernel reads w's rows up to N: they end at n
     const bool grad_pipelined = vec_x && vec_w;
@@ -274,7 +274,8 @@ trt_status trt_linear_xent_bwd(int64_t tokens, int64_t vocab, int64_t width, con
       b.live = &head->live;
       b.factor = &head->factor;
       b.g_cols = (int32_t)n8;
-      const bool pipelined = vec_g && tokens * plan.padded * 2 < kExtent;
+      b.halves = plan.halves;
+      const bool pipelined = vec_g && rows256 * plan.padded * 2 < kExtent;
       if (const hipError_t e = trt::launch_xent_weight(b, in_dtype, plan.wide_w, pipelined, st); e != hipSuccess)
         return done(e);
     }
@@ -295,6 +296,7 @@ trt_status trt_linear_xent_bwd(int64_t tokens, int64_t vocab, int64_t width, con
       b.b_bytes = ((n - 1) * ldw + width) * 2;
       b.head = head;
       b.add = v0 > 0;
+      b.halves = plan.halves;
       // the pipelined kernel takes G's zero columns up to a multiple of 8 too,
       // where they are written; W's rows there lie past its extent and read as zero
       const bool pipelined = vec_w && vec_g && (grad_pipelined || n == n8);
@@ -311,7 +313,7 @@ trt_status trt_linear_xent_bwd(int64_t tokens, int64_t vocab, int64_t width, con
     f.sums = sums;
     f.head = head;
     f.place = place;
-    f.weight = weight;
+    f.halves = plan.halves;
     f.dx = dx;
     f.ld = plan.padded;
     f.lddx = lddx;

@@ -8,13 +8,16 @@
 //   dX = G W,  dW = G^T X
 //
 // Forward: the GEMM kernel's tile of z never leaves the registers.  Its
-// epilogue takes each row's maximum and sum of exp(z - maximum) over the
-// tile's columns, one pair per row and tile (8 bytes for 256 logits), and the
-// target's logit where the tile holds it; xent_combine_kernel joins a row's
-// pairs.  Backward, in pieces of the vocabulary: the same product again, whose
-// epilogue turns z into g in the registers and rounds it once to the inputs'
-// type; then the two products of that piece of G.  Bound by the matrix cores
-// from a few hundred tokens on, by reading W below.
+// epilogue takes each row's maximum over the tile's columns and the sum of
+// exp(z - maximum) over all of them but the target, one pair per row and tile (8
+// bytes for 256 logits), and the target's logit where the tile holds it;
+// xent_combine_kernel joins a row's pairs.  With R the sum over the others,
+// loss = log(1 + R / exp(z_target)): a well predicted token's small loss keeps
+// its relative accuracy, which lse - z_target would lose to cancellation.
+// Backward, in pieces of the vocabulary: the same product again, whose epilogue
+// turns z into g in the registers and rounds it once to the inputs' type; then
+// the two products of that piece of G.  Bound by the matrix cores from a few
+// hundred tokens on, by reading W below.
 //
 // Tokens whose target is the ignored one take no part: xent_prep_kernel lists
 // the others, the products' row counts are read from device memory, and A's
@@ -22,15 +25,15 @@
 // half, and whatever X holds at an ignored token (NaN included) reaches
 // nothing.
 //
-// Roundings to 16 bits beside the results' own.  G: with s_t = max(|dloss_t|,
-// |dloss_t + dlse_t|) taken out, |g| <= 2, and the entry that dominates a row,
-// p_target - 1, loses nothing where p_target is small.  s_t comes back in
-// binary32: as a factor of dX's row, and for dW as c = max_t s_t on the whole
-// and s_t / c on X's rows -- exactly 1 for a mean or a sum, where no further
-// rounding happens; with weights that differ from token to token it rounds
-// X's rows once more.  binary16 would lose small probabilities (its smallest
-// value is 2^-24): G is held times 2^14 there, which keeps all its bits down to
-// p = 2^-28.
+// Roundings to 16 bits beside the results' own: G, to the inputs' type.  With c
+// = max_t max(|dloss_t|, |dloss_t + dlse_t|) taken out and put back in
+// binary32, |g| <= 2, and under a mean or a sum the entry that dominates a row,
+// p_target - 1, loses nothing where p_target is small.  Over many tokens G's
+// roundings average out below the results' own; for few (where the products
+// wait for memory anyway) G is held as two rows of 16-bit numbers, the rounded
+// value and what the rounding left, so that nothing is lost to it.  binary16
+// would lose small probabilities (its smallest value is 2^-24): G is held
+// times 2^14 there, which keeps all bits of a g down to 2^-28 of c.
 #pragma once
 
 #include "gemm_dma.hpp"
@@ -134,9 +137,9 @@ struct XentStats {
 #pragma unroll
       for (int i = 0; i < TL::FM; ++i) {
         int left = p.N - n0 - c0;   // columns from the lane's first one on
-        // (made anew for each row: the 32 comparisons with it, kept from row
-        // to row, would take 64 scalar registers)
-        asm volatile("" : "+v"(left));
+        // (made anew for each row: the 32 comparisons with it, kept from row to
+        // row, would take 64 scalar registers)
+        if (EDGE) asm volatile("" : "+v"(left));
         float v[4 * TL::FN];
 #pragma unroll
         for (int j = 0; j < TL::FN; ++j)
@@ -159,22 +162,36 @@ struct XentStats {
     };
     if (n0 + TL::BN > p.N) rows.template operator()<true>();
     else rows.template operator()<false>();
-    // the targets' columns, from the lane's first one on; few waves hold any
+    // The rows whose target lies in the wave's columns (few waves have any):
+    // the target's logit apart, and the sum again without its term.  (In the
+    // loop above, as a choice between every column and -inf, the wide tile
+    // would spill a third of a row: 8192 x 131072 x 4096 6.35 ms, this way 5.95.)
 #pragma unroll
     for (int i = 0; i < TL::FM; ++i) {
       const int row = TL::owner_row(4 * i * TL::FN, lane, wave), m = m0 + row;
-      int64_t v = -1;
-      if (PIPELINED && (LISTED || p.want)) v = reinterpret_cast<const int32_t*>(kept)[row];
-      else if (m < p.M) v = p.want ? p.want[m] : p.target[m];
-      v -= p.col0 + n0 + c0;
-      const int want = m < p.M && v >= 0 && v < 16 * TL::FN && (v & 15) < 4 ? (int)v : -1;
+      int64_t at = -1;
+      if (PIPELINED && (LISTED || p.want)) at = reinterpret_cast<const int32_t*>(kept)[row];
+      else if (m < p.M) at = p.want ? p.want[m] : p.target[m];
+      at -= p.col0 + n0 + c0;   // from the lane's first column on
+      const int want = m < p.M && at >= 0 && at < 16 * TL::FN && (at & 15) < 4 ? (int)at : -1;
       if (__any(want >= 0)) {
-        float at = 0.f;
+        int left = p.N - n0 - c0;
+        asm volatile("" : "+v"(left));
+        f32x2& pair = pairs[wn * TL::BM + row];
+        const float top = pair[0], base = top == -__builtin_inff() ? 0.f : -top * kLog2E;
+        float z = 0.f, sum = 0.f;
 #pragma unroll
         for (int j = 0; j < TL::FN; ++j)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) at = want == 16 * j + e ? acc[i][j][e] : at;
-        if (want >= 0) p.at[m] = at;
+          for (int e = 0; e < 4; ++e) {
+            const float v = acc[i][j][e], term = __builtin_amdgcn_exp2f(__builtin_fmaf(v, kLog2E, base));
+            const bool it = want == 16 * j + e;
+            z = it ? v : z;
+            sum += it || 16 * j + e >= left ? 0.f : term;
+          }
+        if (want >= 0) p.at[m] = z;
+        sum = row_sum(sum);
+        if (lane < 16) pair[1] = sum;
       }
     }
     __syncthreads();
@@ -303,8 +320,25 @@ struct XentGrad {
 #pragma unroll
             for (int i = 0; i < TL::FM; ++i) acc[i][j][e] = 0.f;
     }
-    if constexpr (PIPELINED) store_rows<TL, DT>(p, acc, m0, n0, lane, wave);
-    else epilogue_store<TL>(p, acc, m0, n0, lane, wave);
+    Args q = p;
+    // (few tokens: not on tiles of 256)
+    const bool halves = TL::BM < 256 && p.halves;
+    if (halves) q.ldc = 2 * p.ldc;   // rows 2m and 2m + 1 of G
+    auto store = [&]() __attribute__((always_inline)) {
+      if constexpr (PIPELINED) store_rows<TL, DT>(q, acc, m0, n0, lane, wave);
+      else epilogue_store<TL>(q, acc, m0, n0, lane, wave);
+    };
+    store();
+    if (halves) {
+#pragma unroll
+      for (int i = 0; i < TL::FM; ++i)
+#pragma unroll
+        for (int j = 0; j < TL::FN; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][j][e] -= to_f32<DT>(from_f32<DT>(acc[i][j][e]));
+      q.C = static_cast<uint16_t*>(p.C) + p.ldc;
+      store();
+    }
   }
 };
 
@@ -316,7 +350,7 @@ struct XentInput {
   // Workgroups in order of their slice, then of their tile.
   __device__ static bool begin(Args& p) {
     const int slice = uniform(p.head->slice);
-    p.M = uniform(p.head->live);
+    p.M = uniform(p.head->live) << p.halves;
     p.tiles_m = (p.M + TL_::BM - 1) / TL_::BM;
     const int tiles = p.tiles_m * p.tiles_n;
     const int at = tiles > 0 ? blockIdx.x / (uint32_t)tiles : 0;
@@ -358,7 +392,7 @@ struct XentWeight {
   using Args = XentWeightArgs;
   __device__ static int tile(const Args&) { return blockIdx.x; }
   __device__ static bool begin(Args& p) {
-    p.K = uniform(*p.live);
+    p.K = uniform(*p.live) << p.halves;
     // in 32 bits: below 2^31 where the pipelined kernel runs, and only it asks
     const int rows = p.K > 0 ? p.K - 1 : 0;
     p.a_bytes = uniform((rows * (int)p.lda + p.g_cols) * 2);

@@ -38,6 +38,7 @@ struct XentGradArgs : GemmArgs {   // C: G, of the inputs' type
   const int32_t* list;
   const XentRow* info;     // [live tokens]
   int32_t cols;            // vocabulary entries of the piece; G's columns past them are zero up to N
+  int32_t halves;          // 1: two rows of G to a token, the rounded value and the rest
   int64_t col0;
 };
 
@@ -45,6 +46,7 @@ struct XentGradArgs : GemmArgs {   // C: G, of the inputs' type
 struct XentInputArgs : GemmArgs {
   const XentHead* head;
   int32_t add;             // add to what the sums hold (every piece after the first)
+  int32_t halves;          // as XentGradArgs
 };
 
 // dW over one piece.
@@ -52,6 +54,7 @@ struct XentWeightArgs : GemmArgs {
   const int32_t* live;
   const float* factor;     // c over G's scale
   int32_t g_cols;          // G's columns that are written
+  int32_t halves;          // as XentGradArgs
 };
 
 struct XentPrepArgs {
@@ -67,6 +70,7 @@ struct XentPrepArgs {
   XentHead* head;
   float scale;                 // backward: G's scale
   int32_t width, k, wide;      // backward: dX's product, K of a whole piece
+  int32_t halves;              // backward: as XentGradArgs
 };
 
 struct XentCombineArgs {
@@ -84,10 +88,9 @@ struct XentCombineArgs {
 struct XentRowsArgs {
   XentPrepArgs prep;
   const uint16_t* x;
-  uint16_t* out;
+  uint16_t* out;           // live tokens' rows of x; with halves, each twice
   const float* lse;
   XentRow* info;
-  float* weight;           // s_t over G's scale
   int64_t ldx, ld;
   int32_t width, vocab;
 };
@@ -96,10 +99,10 @@ struct XentInputFinishArgs {
   const float* sums;
   const XentHead* head;
   const int32_t* place;
-  const float* weight;
   void* dx;
   int64_t ld, lddx;
   int32_t width;
+  int32_t halves;
   int32_t vec;             // dx's rows take aligned runs of four
 };
 

@@ -15,6 +15,10 @@ struct XentHead {
   int32_t slices;    // slices of a whole piece
 };
 
+// Tokens up to which G is held in two rows each: together they fit one tile of
+// 128 rows of dX's product, whose time is reading W.
+constexpr int64_t kXentHalvesTokens = 64;
+
 // Largest number of tokens: one workgroup of 256 threads a token in a launch
 // of fewer than 2^32 threads.  Largest width and piece: byte offsets into a
 // tile's rows stay below 2^31.
@@ -100,9 +104,10 @@ struct XentBwdPlan {
   int64_t piece;       // vocabulary entries at a time, a multiple of 64
   int64_t pieces;
   int64_t padded;      // width of X' and of the sums' rows, a multiple of 8
+  bool halves;         // two rows of G (and of X') to a token
   bool wide_g, wide_x, wide_w;   // 256-wide tiles for G, dX and dW
   int64_t most_tiles;            // workgroups of dX's product, for any number of live tokens
-  int64_t head, list, place, weight, info, x, g, sums;   // byte offsets
+  int64_t head, list, place, info, x, g, sums;   // byte offsets
   int64_t bytes;
 };
 
@@ -127,34 +132,35 @@ constexpr XentBwdPlan xent_bwd_plan(int64_t tokens, int64_t vocab, int64_t width
   if (p.piece > round_up(vocab, 64)) p.piece = round_up(vocab, 64);
   p.pieces = (vocab + p.piece - 1) / p.piece;
   p.padded = round_up(width, 8);
+  p.halves = tokens <= kXentHalvesTokens;
+  const int64_t g_rows = tokens << (p.halves ? 1 : 0);   // the most there may be
   p.wide_g = xent_wide(tokens, p.piece);
   // dW of few tokens is all store: twice the workgroups to a unit (16 tokens:
   // 185 us against 168, 512: 417 against 401, 1024: 681 against 690, 32000 x 4096)
   p.wide_w = tokens > 768 && xent_wide(p.piece, width);
-  p.wide_x = tokens > 192 && width > 192;
+  p.wide_x = tokens > 192 && width > 192;   // (more than the tokens of halves)
   // the sums' room and the grid, for whatever number of tokens is live
   const int64_t tile = p.wide_x ? 256 : 128, cols = (width + tile - 1) / tile;
   const int64_t k = p.piece < vocab ? p.piece : vocab;
   int64_t sum_rows = 0;
-  for (int64_t r = 0; r < tokens; r += tile) {
-    const int64_t rows = tokens - r < tile ? tokens : r + tile;
+  for (int64_t r = 0; r < g_rows; r += tile) {
+    const int64_t rows = g_rows - r < tile ? g_rows : r + tile;
     const int64_t s = xent_slices(rows, width, k, p.wide_x);
     const int64_t tiles = ((rows + tile - 1) / tile) * cols;
     if (s * xent_sum_rows(rows) > sum_rows) sum_rows = s * xent_sum_rows(rows);
     if (s * tiles > p.most_tiles) p.most_tiles = s * tiles;
     // from here on there is one slice and both grow with the rows alone: on to
     // the last
-    if (tiles > 512 && rows < tokens) r = (tokens - 1) / tile * tile - tile;
+    if (tiles > 512 && rows < g_rows) r = (g_rows - 1) / tile * tile - tile;
   }
   int64_t at = 0;
   auto take = [&](int64_t n) { const int64_t o = at; at += round_up(n, 256); return o; };
   p.head = take(sizeof(XentHead));
   p.list = take(tokens * 4);
   p.place = take(tokens * 4);
-  p.weight = take(tokens * 4);
   p.info = take(tokens * 16);
-  p.x = take(tokens * p.padded * 2);
-  p.g = take(tokens * p.piece * 2);
+  p.x = take(g_rows * p.padded * 2);
+  p.g = take(g_rows * p.piece * 2);
   p.sums = take(sum_rows * p.padded * 4);
   p.bytes = at;
   return p;

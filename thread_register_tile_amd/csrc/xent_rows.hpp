@@ -91,7 +91,7 @@ __global__ __launch_bounds__(kPrepThreads) void xent_prep_kernel(XentPrepArgs a)
       for (int off = 8; off >= 1; off >>= 1) c = __builtin_fmaxf(c, __shfl_xor(c, off));
       // the number of slices of dX's product: lane s - 1 weighs s of them, the
       // least cost and of those the least number is taken
-      const uint32_t tiles = xent_input_tiles(base, a.width, a.wide != 0);
+      const uint32_t tiles = xent_input_tiles((int64_t)base << a.halves, a.width, a.wide != 0);
       const uint32_t mine = lane < kXentMostSlices ? lane + 1 : 1;
       uint64_t cost = xent_slice_cost(mine, tiles, a.k, a.wide != 0);
       uint32_t best = mine;
@@ -145,70 +145,80 @@ __global__ __launch_bounds__(256) void xent_combine_kernel(XentCombineArgs a) {
   if (j != 0 || m >= rows) return;
   const int64_t tok = a.list ? a.list[m] : m;
   const int64_t target = a.target[tok];
-  const float rest = logf(sum);
   if (target == a.ignore) {
     a.loss[tok] = 0.f;
     a.lse[tok] = 0.f;
     return;
   }
-  // a target outside the vocabulary has no loss: NaN, where it can be seen
+  // sum: over every entry but the target (top may be the target's).  A target
+  // outside the vocabulary has no loss: NaN, where it can be seen
+  const float inf = __builtin_inff(), nan = __builtin_nanf("");
   const bool known = target >= 0 && target < a.vocab;
-  a.loss[tok] = known ? (top - a.at[m]) + rest : __builtin_nanf("");
-  a.lse[tok] = top + rest;
+  const float z = known ? a.at[m] : -inf;
+  const float up = __builtin_fmaxf(top, z);
+  const float base = up == -inf ? 0.f : up;
+  a.lse[tok] = up + logf(sum * expf(top - base) + expf(z - base));
+  const float d = top - z;
+  float loss;
+  if (top == -inf) loss = sum == 0.f && z > -inf && z < inf ? 0.f : nan;   // no other entry
+  else if (d < 60.f) loss = log1pf(sum * expf(d));
+  else loss = d + logf(sum + expf(-d));
+  a.loss[tok] = known && z < inf ? loss : nan;
 }
 
-// The live tokens' rows: X' = X s_t / c, packed with a row of `ld` elements
-// (zero past the width), and what the gradient's epilogue needs of each.
+// The live tokens' rows, packed with a row of `ld` elements (zero past the
+// width), and what the gradient's epilogue needs of each token.
 template <int DT>
 __global__ __launch_bounds__(256) void xent_rows_kernel(XentRowsArgs a) {
   using C = RowChunk<DT>;
   const int m = blockIdx.x;
   if (m >= a.prep.head->live) return;   // the whole workgroup
   const int tok = a.prep.list[m];
-  float dl, both;
-  const float s = xent_weight(a.prep, tok, dl, both);   // not zero: the token is live
-  const float c = a.prep.head->c;
-  const float ratio = s == c ? 1.f : s / c;   // exactly 1 for equal weights
   if (threadIdx.x == 0) {
+    float dl, both;
+    xent_weight(a.prep, tok, dl, both);
+    const float c = a.prep.head->c;   // not zero: the token is live
     const int64_t target = a.prep.target[tok];
     const bool known = target >= 0 && target < a.vocab;
     // a target outside the vocabulary: a NaN row, where it can be seen.  The
-    // quotients are exactly 1 or -1 without a dlse
-    a.info[m] = XentRow{known ? both / s : __builtin_nanf(""), dl / s, a.lse[tok] * kLog2E,
+    // quotients are exactly 1 or -1 for equal dloss and no dlse
+    a.info[m] = XentRow{known ? both / c : __builtin_nanf(""), dl / c, a.lse[tok] * kLog2E,
                         known ? (int32_t)target : -1};
-    a.weight[m] = s / a.prep.scale;
   }
   const uint16_t* src = a.x + (int64_t)tok * a.ldx;
-  uint16_t* dst = a.out + (int64_t)m * a.ld;
+  uint16_t* dst = a.out + ((int64_t)m << a.prep.halves) * a.ld;
   for (int i = C::VEC * threadIdx.x; i < a.ld; i += C::VEC * 256) {
     u32x4 v = {0u, 0u, 0u, 0u};
     if (i < a.width) v = C::load(src, i, a.width);
-    if (ratio != 1.f) {
-#pragma unroll
-      for (int w = 0; w < 4; ++w)
-        v[w] = pack2_f32<DT>(C::elem(v, 2 * w) * ratio, C::elem(v, 2 * w + 1) * ratio);
-    }
     *reinterpret_cast<u32x4*>(dst + i) = v;
+    if (a.prep.halves) *reinterpret_cast<u32x4*>(dst + a.ld + i) = v;
   }
 }
 
-// dX from the slices' sums: row t is its weight times the sum over the slices
-// in order, or zeros for an ignored token.
+// dX from the slices' sums: a row is c times the sum over the slices in order
+// (with halves, of its two rows in each), or zeros for a token that is not live.
 template <int OT>
 __global__ __launch_bounds__(256) void xent_input_finish_kernel(XentInputFinishArgs a) {
   using O = Out<OT>;
   const int64_t t = blockIdx.x;
   const int m = a.place[t];
-  const float w = m < 0 ? 0.f : a.weight[m];
+  const float f = a.head->factor;
   const int slices = a.head->slices;
-  const int64_t stride = xent_sum_rows(a.head->live) * a.ld;
-  for (int i = 4 * threadIdx.x; i < a.width; i += 1024) {
+  const int64_t stride = xent_sum_rows((int64_t)a.head->live << a.halves) * a.ld;
+  const int step = 4 * blockDim.x * gridDim.y;
+  for (int i = 4 * (blockIdx.y * blockDim.x + threadIdx.x); i < a.width; i += step) {
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
     if (m >= 0) {   // the sums' rows are padded to whole eights
-      const float* p = a.sums + (int64_t)m * a.ld + i;
+      const float* p = a.sums + ((int64_t)m << a.halves) * a.ld + i;
+      if (a.halves) {
 #pragma unroll 8
-      for (int s = 0; s < slices; ++s) v += *reinterpret_cast<const f32x4*>(p + s * stride);
-      v *= w;
+        for (int s = 0; s < slices; ++s)
+          v += *reinterpret_cast<const f32x4*>(p + s * stride) + *reinterpret_cast<const f32x4*>(p + s * stride + a.ld);
+      } else {
+#pragma unroll 8
+        for (int s = 0; s < slices; ++s) v += *reinterpret_cast<const f32x4*>(p + s * stride);
+      }
+      v *= f;
     }
     const int64_t at = t * a.lddx + i;
     if (a.vec && i + 4 <= a.width) {

@@ -88,14 +88,17 @@ __global__ __launch_bounds__(kXentStreamThreads) void xent_stream_kernel(XentSta
   // a wave for each token
   if (wave >= T || wave >= p.M) return;
   const int n = n0 + lane;
-  const float z = n < p.N ? logits[wave < T ? wave : 0][lane] : -__builtin_inff();
-  float top = z;
+  const float z = n < p.N ? logits[wave][lane] : -__builtin_inff();
+  // the target's logit is kept apart from the sum
+  const bool target = p.target[wave] == n;
+  if (target) p.at[wave] = z;
+  const float other = target ? -__builtin_inff() : z;
+  float top = other;
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, off));
   const float base = top == -__builtin_inff() ? 0.f : -top * kLog2E;
-  const float sum = wave_sum(__builtin_amdgcn_exp2f(__builtin_fmaf(z, kLog2E, base)));
+  const float sum = wave_sum(__builtin_amdgcn_exp2f(__builtin_fmaf(other, kLog2E, base)));
   if (lane == 0) p.part[(int64_t)blockIdx.x * p.ldp + wave] = f32x2{top, sum};
-  if (p.target[wave] == n) p.at[wave] = z;
 }
 
 }  // namespace trt
