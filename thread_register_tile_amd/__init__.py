@@ -591,7 +591,8 @@ def _device(first, **others):
 def _on(dev, status_of):
     """status_of(stream) with dev current (a launch goes to the current device)."""
     torch = _torch()
-    stream = torch.cuda.current_stream(dev).cuda_stream or None
+    # (the handle itself: making a Stream object of it takes 1.7 us of a call's 10)
+    stream = torch._C._cuda_getCurrentRawStream(dev.index) or None
     if torch.cuda.current_device() == dev.index:
         return _check(status_of(stream))
     with torch.cuda.device(dev):
@@ -631,10 +632,19 @@ def _like(out, t, name):
     """out, or a new contiguous tensor of t's shape and dtype."""
     torch = _torch()
     if out is None:
-        return torch.empty(t.shape, dtype=t.dtype, device=t.device)
+        return torch.empty_like(t, memory_format=torch.contiguous_format)
     if out.shape != t.shape or out.dtype != t.dtype:
         raise TrtError(ERR_SIZE, f"{name} must be {list(t.shape)} of {t.dtype}")
     return out
+
+
+def _workspace(ws, need, like):
+    """ws, or a new workspace of need bytes on like's device."""
+    if ws is None:
+        return like.new_empty(need, dtype=_torch().uint8)
+    if not ws.is_contiguous():
+        raise TrtError(ERR_STRIDE, "the workspace must be contiguous")
+    return ws
 
 
 def layernorm(x, gamma=None, beta=None, *, eps=1e-5, out=None):
@@ -649,10 +659,11 @@ def layernorm(x, gamma=None, beta=None, *, eps=1e-5, out=None):
     param = next((t.dtype for t in (gamma, beta) if t is not None), x.dtype)
     pdt = next((_dtype_code(t) for t in (gamma, beta) if t is not None), _dtype_code(x))
     g, b = _vector(gamma, "gamma", cols, param), _vector(beta, "beta", cols, param)
+    ldy = max(cols, 1) if out is None else _rows(out, "out")[2]
     out = _like(out, x, "out")
     dev = _device(x, gamma=gamma, beta=beta, out=out)
     _on(dev, lambda s: lib().trt_layernorm(rows, cols, x.data_ptr(), ldx, g, b, eps,
-                                           out.data_ptr(), _rows(out, "out")[2],
+                                           out.data_ptr(), ldy,
                                            _dtype_code(x), pdt, s))
     return out
 
@@ -682,25 +693,25 @@ def layernorm_bwd(dy, x, gamma=None, *, eps=1e-5, params=True, dx=None, dgamma=N
     param = next((t for t in (gamma, dgamma, dbeta) if t is not None), None)
     pdtype = torch.float32 if param is None else param.dtype
     pdt = F32 if param is None else _dtype_code(param)
+    lddx = max(cols, 1) if dx is None else _rows(dx, "dx")[2]
     dx = _like(dx, x, "dx")
     if params:
         need = layernorm_bwd_workspace_size(rows, cols, _dtype_code(x))
         if dgamma is None:
-            dgamma = torch.empty(cols, dtype=pdtype, device=x.device)
+            dgamma = x.new_empty(cols, dtype=pdtype)
         if dbeta is None:
-            dbeta = torch.empty(cols, dtype=pdtype, device=x.device)
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+            dbeta = torch.empty_like(dgamma)
+        workspace = _workspace(workspace, need, x)
     else:
         dgamma = dbeta = workspace = None
     g, dg, db = (_vector(t, name, cols, pdtype) for t, name in
                  ((gamma, "gamma"), (dgamma, "dgamma"), (dbeta, "dbeta")))
     dev = _device(x, dy=dy, gamma=gamma, dx=dx, dgamma=dgamma, dbeta=dbeta, workspace=workspace)
-    ws, wsb = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    ws, wsb = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
     _on(dev, lambda s: lib().trt_layernorm_bwd(rows, cols, dy.data_ptr(), _rows(dy, "dy")[2],
                                                x.data_ptr(), ldx, g, eps, dx.data_ptr(),
-                                               _rows(dx, "dx")[2], dg, db, _dtype_code(x), pdt,
-                                               ws or None, wsb, s))
+                                               lddx, dg, db, _dtype_code(x), pdt,
+                                               ws, wsb, s))
     return dx, dgamma, dbeta
 
 
@@ -747,14 +758,12 @@ def _tokens_out(t, name, like):
     """t, or a new float32 tensor of like's shape."""
     torch = _torch()
     if t is None:
-        return torch.empty(like.shape, dtype=torch.float32, device=like.device)
+        return torch.empty_like(like, dtype=torch.float32)
     if t.shape != like.shape or t.dtype != torch.float32 or not t.is_contiguous():
         raise TrtError(ERR_SIZE, f"{name} must be contiguous float32 of shape {list(like.shape)}")
     return t
 
 
-def _workspace(ws, need, device):
-    return _torch().empty(need, dtype=_torch().uint8, device=device) if ws is None else ws
 
 
 def linear_xent_workspace_size(tokens, vocab, width) -> int:
@@ -775,13 +784,13 @@ def linear_xent(x, w, target, *, ignore_index=-100, loss=None, lse=None, workspa
     synchronisation.
     """
     tokens, vocab, width, ldx, ldw = _xent_inputs(x, w, target)
-    workspace = _workspace(workspace, linear_xent_workspace_size(tokens, vocab, width), x.device)
+    workspace = _workspace(workspace, linear_xent_workspace_size(tokens, vocab, width), x)
     loss, lse = _tokens_out(loss, "loss", target), _tokens_out(lse, "lse", target)
     dev = _device(x, w=w, target=target, loss=loss, lse=lse, workspace=workspace)
     _on(dev, lambda s: lib().trt_linear_xent(tokens, vocab, width, x.data_ptr(), ldx, w.data_ptr(), ldw,
                                              target.data_ptr(), ignore_index, loss.data_ptr(),
                                              lse.data_ptr(), _dtype_code(x), workspace.data_ptr(),
-                                             workspace.numel() * workspace.element_size(), s))
+                                             workspace.nbytes, s))
     return loss, lse
 
 
@@ -818,18 +827,18 @@ def linear_xent_bwd(x, w, target, lse, dloss, dlse=None, *, ignore_index=-100, n
         if not need:
             return None, 0
         if t is None:
-            t = torch.empty(like.shape, dtype=odt, device=like.device)
+            t = torch.empty_like(like, dtype=odt, memory_format=torch.contiguous_format)
         elif t.shape != like.shape or t.dtype != odt:
             raise TrtError(ERR_SIZE, f"{name} must be {list(like.shape)} of {odt}")
         return t, _rows(t, name)[2]
 
     (dx, lddx), (dw, lddw) = output(dx, x, need_dx, "dx"), output(dw, w, need_dw, "dw")
     out = next((t for t in (dx, dw) if t is not None), x)
-    workspace = _workspace(workspace, linear_xent_bwd_workspace_size(tokens, vocab, width, piece), x.device)
+    workspace = _workspace(workspace, linear_xent_bwd_workspace_size(tokens, vocab, width, piece), x)
     dev = _device(x, w=w, target=target, lse=lse, dloss=dloss, dlse=dlse, dx=dx, dw=dw, workspace=workspace)
     _on(dev, lambda s: lib().trt_linear_xent_bwd(
         tokens, vocab, width, x.data_ptr(), ldx, w.data_ptr(), ldw, target.data_ptr(), ignore_index,
         lse.data_ptr(), dl, dl_inc, de, de_inc, None if dx is None else dx.data_ptr(), lddx,
         None if dw is None else dw.data_ptr(), lddw, _dtype_code(x), _dtype_code(out), piece,
-        workspace.data_ptr(), workspace.numel() * workspace.element_size(), s))
+        workspace.data_ptr(), workspace.nbytes, s))
     return dx, dw
