@@ -145,6 +145,14 @@ def test_longest_rows(cols, dtype):
     run_case(3, cols, dtype, dtype, seed=cols)
 
 
+@pytest.mark.parametrize("dtype,cols", [(torch.bfloat16, 16379), (torch.float16, 20490), (torch.bfloat16, 24577),
+                                        (torch.float32, 8201), (torch.float32, 12289)],
+                         ids=lambda v: NAMES.get(v, v))
+def test_long_rows_in_turns(cols, dtype):
+    # each workgroup takes several rows, the last ones fewer
+    run_case(515, cols, dtype, torch.float32, seed=cols)
+
+
 @pytest.mark.parametrize("dtype", DTYPES, ids=NAMES.get)
 @pytest.mark.parametrize("rows", [1, 2, 3, 4, 31, 257, 4099])
 def test_row_counts(rows, dtype):

@@ -217,21 +217,24 @@ __global__ __launch_bounds__(NormShape<W>::THREADS) void layernorm_kernel(NormAr
 // compute unit: the fewer slices, the fewer bytes beside the rows' own (with
 // workgroups of one row, two to a unit, the slices were 8 % of the traffic of
 // 16384 rows of 8192, and 8 % of the time).
-// AHEAD: the next row is loaded ahead and gamma kept in registers; rows of 16
-// waves leave none for that.
+// AHEAD, KEPT: the next row is loaded ahead, and gamma kept in registers, where
+// a lane's packed row and sums leave room for it (2000 rows of 16384 bf16
+// elements: 87 us without, 66 with).
 // (Too few rows to give every unit one of 16 waves take the forward pass's
 // smaller ones.)
 template <int DT, int PDT, int W, int K, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void layernorm_bwd_kernel(NormArgs a) {
   using C = RowChunk<DT>;
   constexpr int VEC = C::VEC, LANES = 64 * W, GROUPS = WAVES / W;
-  constexpr bool AHEAD = K <= 2 && W < 16;
+  constexpr int ROOM = WAVES == 16 ? 84 : 176;   // of 128 and 256 registers
+  constexpr int HELD = K * (8 + 2 * VEC);        // x, dy and the sums
+  constexpr bool AHEAD = HELD + 8 * K <= ROOM, KEPT = AHEAD && HELD + 8 * K + VEC * K <= ROOM;
   __shared__ float buf[2][16][4];
   __shared__ float fold[GROUPS > 1 ? GROUPS : 1][GROUPS > 1 ? LANES * VEC * K : 1];
   // the wave's index in a scalar register: row addresses are then scalar too
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wave = w % W, grp = w / W;
-  const int me = 64 * wave + (threadIdx.x & 63);
+  int me = 64 * wave + (threadIdx.x & 63);
   const int n = a.cols;
   const float inv = 1.f / (float)a.cols;
   const int64_t step = (int64_t)gridDim.x * GROUPS;
@@ -246,7 +249,7 @@ __global__ __launch_bounds__(64 * WAVES) void layernorm_bwd_kernel(NormArgs a) {
   };
 
   u32x4 nx[AHEAD ? K : 1], ny[AHEAD ? K : 1];
-  float kept[AHEAD ? K : 1][VEC];
+  float kept[KEPT ? K : 1][VEC];
   if constexpr (AHEAD) {
 #pragma unroll
     for (int k = 0; k < K; ++k) nx[k] = ny[k] = u32x4{0u, 0u, 0u, 0u};
@@ -254,6 +257,8 @@ __global__ __launch_bounds__(64 * WAVES) void layernorm_bwd_kernel(NormArgs a) {
       load(nx, a.x, a.ldx, r);
       load(ny, a.dy, a.lddy, r);
     }
+  }
+  if constexpr (KEPT) {
 #pragma unroll
     for (int k = 0; k < K; ++k) load_params<PDT>(a.gamma, col(k), n, 1.f, kept[k]);
   }
@@ -266,6 +271,9 @@ __global__ __launch_bounds__(64 * WAVES) void layernorm_bwd_kernel(NormArgs a) {
   // every wave takes as many turns as the workgroup's first row needs; one
   // past the last row works on zeros and keeps nothing
   for (int64_t r0 = (int64_t)blockIdx.x * GROUPS; r0 < a.rows; r0 += step, r += step) {
+    // addresses and column tests made anew for each pass over a row: kept they
+    // would take a third of the registers
+    if constexpr (K * VEC > 32) asm volatile("" : "+v"(me));
     const bool live = r < a.rows;
     u32x4 x[K], y[K];
     if constexpr (AHEAD) {
@@ -292,13 +300,14 @@ __global__ __launch_bounds__(64 * WAVES) void layernorm_bwd_kernel(NormArgs a) {
     keep_packed(x);
     const float m = rounded(s[0] * inv);
     auto gamma_of = [&](int k, float (&g)[VEC]) {
-      if constexpr (AHEAD) {
+      if constexpr (KEPT) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) g[e] = kept[k][e];
       } else {
         load_params<PDT>(a.gamma, col(k), n, 1.f, g);
       }
     };
+    if constexpr (K * VEC > 32) asm volatile("" : "+v"(me));
     float q[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -321,6 +330,7 @@ __global__ __launch_bounds__(64 * WAVES) void layernorm_bwd_kernel(NormArgs a) {
     const float c1 = q[2] * inv;
     const float c2 = rstd * (q[3] * inv - dbar * c1);   // mean(u h)
     if (!live) continue;
+    if constexpr (K * VEC > 32) asm volatile("" : "+v"(me));
     char* p = static_cast<char*>(a.out) + r * a.ldo * (int64_t)sizeof(typename C::Elem);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
