@@ -13,13 +13,16 @@ namespace {
 // several rows to a workgroup.  Longer rows take 4, 8 and 16 waves, so that a
 // lane holds few chunks.  The backward pass keeps two running sums per element
 // of them in registers: it stays at 8 waves, whose lanes have 256 (1000 rows of
-// 8200 binary32 elements: 78 us in 16 waves of 128 registers, 33 in 8).
+// 8200 binary32 elements: 78 us in 16 waves of 128 registers, 33 in 8), and
+// with as many gives a wave rows of up to 256 chunks (8192 rows of 2048 bf16
+// elements: 30.5 us in four waves a row, 25 in one; 64000 rows 181 and 148).
 struct Shape {
   int w, k;
 };
 constexpr Shape shape_of(int64_t chunks, bool backward) {
   if (chunks <= 64) return {1, 1};
   if (chunks <= 128) return {1, 2};
+  if (backward && chunks <= 256) return {1, chunks <= 192 ? 3 : 4};
   if (chunks <= 256) return {4, 1};
   if (chunks <= 512) return {4, 2};
   if (chunks <= 768 && !backward) return {4, 3};
@@ -47,11 +50,17 @@ constexpr int forward_most() { return W == 1 ? 8 : 16 / W; }
 template <int DT, bool BACKWARD, class F>
 auto with_shape(int64_t cols, F&& f) {
   const Shape s = shape_of((cols + RowChunk<DT>::VEC - 1) / RowChunk<DT>::VEC, BACKWARD);
+  if constexpr (BACKWARD) {
+    if (s.w == 1 && s.k == 3) return f.template operator()<1, 3>();
+    if (s.w == 1 && s.k == 4) return f.template operator()<1, 4>();
+  }
   if (s.w == 1) return s.k == 1 ? f.template operator()<1, 1>() : f.template operator()<1, 2>();
   if (s.w == 4) {
-    if constexpr (!BACKWARD)
+    if constexpr (!BACKWARD) {
+      if (s.k == 1) return f.template operator()<4, 1>();
       if (s.k == 3) return f.template operator()<4, 3>();
-    return s.k == 1 ? f.template operator()<4, 1>() : f.template operator()<4, 2>();
+    }
+    return f.template operator()<4, 2>();
   }
   if constexpr (BACKWARD) {
     if (s.k == 2) return f.template operator()<8, 2>();
@@ -63,10 +72,10 @@ auto with_shape(int64_t cols, F&& f) {
   }
 }
 
-// Waves of a backward workgroup: 16, rows of which the registers allow it and
-// where such workgroups fill the 256 units; else as the forward pass has them.
+// Waves of a backward workgroup: 16, or 8 where a lane holds three chunks and
+// more, if such workgroups fill the 256 units; else as the forward pass has them.
 template <int W, int K>
-constexpr int kBwdWaves = W == 8 && K >= 4 ? 8 : 16;
+constexpr int kBwdWaves = K >= 3 ? 8 : 16;
 template <int W, int K>
 bool bwd_large(int64_t rows) {
   return (rows + kBwdWaves<W, K> / W - 1) / (kBwdWaves<W, K> / W) >= 256;
