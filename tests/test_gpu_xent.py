@@ -313,6 +313,36 @@ def test_nonfinite_logits_stay_alone():
         assert loss[[3, T - 1]].isnan().all() and torch.equal(loss[rest], clean[rest])
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("T", [40, 300])
+def test_nonfinite_upstream_gradients_stay_alone(T, dtype):
+    # a token whose dloss overflowed takes its own row of dX and dW, no other row
+    c = Case(T, 500, 64, dtype, seed=16, weights="each")
+    c.dloss[3] = 0.5 * c.dloss.abs().max()
+    clean, _ = c.backward()
+    rest = torch.arange(T, device="cuda") != 3
+    for bad in ("inf", "-inf", "nan"):
+        c.dloss[3] = float(bad)
+        dx, dw = c.backward()
+        assert not dx[3].isfinite().any() and torch.equal(dx[rest], clean[rest])
+        assert not dw.isfinite().all()
+    c.dloss[:] = float("inf")
+    dx, _ = c.backward()
+    assert not dx.isfinite().any()
+
+
+@pytest.mark.parametrize("T", [40, 300])
+def test_subnormal_upstream_gradients(T):
+    # powers of two: every step but the last product is the same but for its
+    # exponent, and that one rounds to a multiple of 2^-149
+    c = Case(T, 500, 64, BF16, seed=17)
+    c.dloss.fill_(1.0)
+    one, _ = c.backward(out_dtype=torch.float32)
+    c.dloss.fill_(2.0 ** -130)
+    dx, dw = c.backward(out_dtype=torch.float32)
+    assert ((dx.double() - one.double() * 2.0 ** -130).abs() <= 2.0 ** -150).all() and dw.isfinite().all()
+
+
 def test_minus_infinity_logits():
     # a vocabulary entry whose logit is -inf has probability zero
     x = torch.zeros(5, 16, dtype=F16, device="cuda")

@@ -12,7 +12,7 @@ namespace trt {
 // tokens of a block of 8192, waves scan their threads' counts by shuffles and
 // the workgroup its waves' through LDS.  Backward, a token whose upstream
 // gradients are both zero is not live either, and the kernel takes c, the
-// largest s_t.  Forward, it writes the ignored tokens' results.
+// largest finite s_t.  Forward, it writes the ignored tokens' results.
 constexpr int kPrepThreads = 1024, kPrepEach = 8;
 
 __device__ __forceinline__ float xent_weight(const XentPrepArgs& a, int64_t t, float& dl, float& both) {
@@ -46,7 +46,9 @@ __global__ __launch_bounds__(kPrepThreads) void xent_prep_kernel(XentPrepArgs a)
     for (int e = 0; e < kPrepEach; ++e) {
       const bool live = first + e < a.tokens && target[e] != a.ignore && s[e] != 0.f;
       keep |= live ? 1u << e : 0u;
-      c = live ? __builtin_fmaxf(c, s[e]) : c;
+      // (of the finite ones: a token whose gradient is not takes its own row of dX
+      // with it, and dW, but no other row)
+      c = live && s[e] <= __FLT_MAX__ ? __builtin_fmaxf(c, s[e]) : c;
     }
     int upto = __popc(keep);   // inclusive count over the wave's lanes
 #pragma unroll
@@ -101,6 +103,8 @@ __global__ __launch_bounds__(kPrepThreads) void xent_prep_kernel(XentPrepArgs a)
         const uint32_t its = __shfl_xor(best, off);
         if (other < cost || (other == cost && its < best)) cost = other, best = its;
       }
+      // (the quotients by c and c over G's scale stay normal numbers)
+      c = __builtin_fmaxf(c, 0x1p-110f);
       if (lane == 0) {
         const uint32_t slice = xent_slice(best, a.k);
         *a.head = XentHead{base, c, c / a.scale, (int32_t)slice, (int32_t)((a.k + slice - 1) / slice)};
@@ -177,7 +181,7 @@ __global__ __launch_bounds__(256) void xent_rows_kernel(XentRowsArgs a) {
   if (threadIdx.x == 0) {
     float dl, both;
     xent_weight(a.prep, tok, dl, both);
-    const float c = a.prep.head->c;   // not zero: the token is live
+    const float c = a.prep.head->c;   // never zero
     const int64_t target = a.prep.target[tok];
     const bool known = target >= 0 && target < a.vocab;
     // a target outside the vocabulary: a NaN row, where it can be seen.  The
