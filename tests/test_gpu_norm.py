@@ -298,3 +298,20 @@ def test_capture_and_replay():
         torch.cuda.synchronize()
         assert torch.equal(y, trt.layernorm(x, g, b))
         assert all(torch.equal(p, q) for p, q in zip((dx, dg, db), trt.layernorm_bwd(dy, x, g)))
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=NAMES.get)
+def test_rows_far_apart(dtype):
+    # rows 16 or 32 MB apart, offsets past 2^32 bytes: the same results as from
+    # packed rows
+    rows, cols, ld = 300, 520, 8_000_000
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    x, dy = (torch.randn(rows, cols, generator=gen, device="cuda").to(dtype) for _ in range(2))
+    gamma = torch.randn(cols, generator=gen, device="cuda")
+    far_x, far_dy, out = (torch.empty(rows * ld, dtype=dtype, device="cuda").view(rows, ld)[:, :cols] for _ in range(3))
+    far_x.copy_(x)
+    far_dy.copy_(dy)
+    assert torch.equal(trt.layernorm(far_x, gamma, out=out), trt.layernorm(x, gamma))
+    got = trt.layernorm_bwd(far_dy, far_x, gamma, dx=out)
+    for a, b in zip(got, trt.layernorm_bwd(dy, x, gamma)):
+        assert torch.equal(a, b)

@@ -476,3 +476,61 @@ def test_norm_head_loss_and_back_in_one_graph():
     h, r = norm_ref.stats(f64(x), 1e-5)
     most = np.abs(dh * f64(gamma)).max(1, keepdims=True)
     check(dxn, want, half_step(want, BF16) + 4 * r * 2.0 ** -8 * 3 * most * (1 + np.abs(h).max(1, keepdims=True)), "chain")
+
+
+# ---- offsets past 2^31 and 2^32 bytes --------------------------------------------------
+
+def test_rows_far_apart():
+    # rows of x and w 16 MB apart: offsets of 4.8 and 8 GB
+    c = Case(300, 500, 64, BF16, seed=31, pad=8_000_000, ignored=0.3, weights="each")
+    c.check_forward()
+    c.check_backward()
+
+
+@pytest.fixture(scope="module")
+def large_weight():
+    # 4.4 GB of W, entries of a fixed size each, the last vocabulary entries as any other
+    gen = torch.Generator(device="cuda").manual_seed(32)
+    w = torch.empty(540_000, 4096, dtype=BF16, device="cuda")
+    for v in range(0, len(w), 60_000):
+        w[v:v + 60_000] = torch.randn(60_000, 4096, generator=gen, device="cuda") / 64
+    yield w
+    del w
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("T", [3, 40, 200])
+def test_large_weight(large_weight, T):
+    w = large_weight
+    V, D = w.shape
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    x = (2 * torch.randn(T, D, generator=gen, device="cuda")).to(BF16)
+    target = torch.randint(0, V, (T,), generator=gen, device="cuda")
+    target[0], target[1], target[2] = V - 1, 262_143, 262_145
+    dloss = torch.full((T,), 1.0 / T, device="cuda")
+    loss, lse = trt.linear_xent(x, w, target)
+    dx, dw = trt.linear_xent_bwd(x, w, target, lse, dloss, out_dtype=torch.float32)
+    steps = [slice(v, min(v + 60_000, V)) for v in range(0, V, 60_000)]
+    z = torch.cat([x.double() @ w[s].double().T for s in steps], 1)
+    want = torch.logsumexp(z, 1)
+    S = max(float((x.abs().double() @ w[s].abs().double().T).max()) for s in steps)
+    dz = (D + 2) * U * S
+    tol = dz + U * (4 * float(z.abs().max()) + 4 * float(want.max()) + 8 + 64 + 3 * V / 64)
+    assert ((lse.double() - want).abs() <= tol).all()
+    assert ((loss.double() - (want - z.gather(1, target[:, None])[:, 0])).abs() <= 2 * tol).all()
+    # G is off by half a step (its square with two rows a token) and by lse's and
+    # the logits' errors; dX's sums run over V, dW's over T
+    p = torch.exp(z - want[:, None])
+    g = p / T
+    g[torch.arange(T), target] -= 1.0 / T
+    h = torch.finfo(BF16).eps / 2
+    dg = (h * h if T <= 64 else h) * g.abs() + 2 * tol * p / T
+    rdx, tdx = torch.zeros(T, D, dtype=torch.float64, device="cuda"), torch.zeros(T, D, dtype=torch.float64, device="cuda")
+    for s in steps:
+        ws = w[s].double()
+        rdx += g[:, s] @ ws
+        tdx += dg[:, s] @ ws.abs() + U * (2 * V + 4) * (g[:, s].abs() @ ws.abs())
+        rdw = g[:, s].T.contiguous() @ x.double()
+        tdw = dg[:, s].T.contiguous() @ x.abs().double() + U * (2 * T + 5) * (g[:, s].abs().T.contiguous() @ x.abs().double())
+        assert ((dw[s].double() - rdw).abs() <= tdw + 2.0 ** -140).all(), s
+    assert ((dx.double() - rdx).abs() <= tdx + U * rdx.abs()).all()

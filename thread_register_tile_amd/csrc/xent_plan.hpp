@@ -113,11 +113,13 @@ struct XentBwdPlan {
 
 // The piece the library chooses: G of at most 2^28 elements (512 MiB), but
 // 8192 entries at least, so that adding dX's sums (8 bytes per token, width
-// and piece) stays small beside the piece's products; never 2 GiB or more.
-constexpr int64_t xent_piece(int64_t tokens, int64_t vocab) {
+// and piece) stays small beside the piece's products; neither G nor the
+// piece's rows of W are ever 2 GiB or more.
+constexpr int64_t xent_piece(int64_t tokens, int64_t vocab, int64_t width) {
   int64_t most = (int64_t(1) << 28) / tokens;
   if (most < 8192) most = 8192;
-  const int64_t limit = ((int64_t(1) << 30) - 4096) / round_up(tokens, 256);
+  const int64_t rows = tokens > width ? tokens : width;
+  const int64_t limit = ((int64_t(1) << 30) - 4096) / round_up(rows, 256);
   if (most > limit) most = limit;
   if (most > kXentMaxPiece) most = kXentMaxPiece;
   if (most < 256) most = 256;
@@ -128,7 +130,7 @@ constexpr int64_t xent_piece(int64_t tokens, int64_t vocab) {
 
 constexpr XentBwdPlan xent_bwd_plan(int64_t tokens, int64_t vocab, int64_t width, int64_t piece) {
   XentBwdPlan p{};
-  p.piece = piece > 0 ? piece : xent_piece(tokens, vocab);
+  p.piece = piece > 0 ? piece : xent_piece(tokens, vocab, width);
   if (p.piece > round_up(vocab, 64)) p.piece = round_up(vocab, 64);
   p.pieces = (vocab + p.piece - 1) / p.piece;
   p.padded = round_up(width, 8);
