@@ -534,3 +534,55 @@ def test_large_weight(large_weight, T):
         tdw = dg[:, s].T.contiguous() @ x.abs().double() + U * (2 * T + 5) * (g[:, s].abs().T.contiguous() @ x.abs().double())
         assert ((dw[s].double() - rdw).abs() <= tdw + 2.0 ** -140).all(), s
     assert ((dx.double() - rdx).abs() <= tdx + U * rdx.abs()).all()
+
+
+# ---- calls at once, graphs that share a workspace --------------------------------------
+
+def test_two_streams_at_once():
+    cases = [Case(300, 9000, 264, BF16, seed=41, ignored=0.2), Case(60, 20000, 136, BF16, seed=42)]
+
+    def step(c):
+        loss, lse = trt.linear_xent(c.x, c.w, c.target, ignore_index=IGNORE)
+        return (loss, lse) + trt.linear_xent_bwd(c.x, c.w, c.target, lse, c.dloss, ignore_index=IGNORE)
+
+    want = [step(c) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[], []]
+    for _ in range(5):
+        for c, st, g in zip(cases, streams, got):
+            with torch.cuda.stream(st):
+                g.append(step(c))
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        for one in g:
+            assert all(torch.equal(a, b) for a, b in zip(one, w))
+
+
+def test_two_graphs_share_a_workspace():
+    T, V, D = 200, 5000, 128
+    cases = [Case(T, V, D, BF16, seed=s, ignored=0.3) for s in (43, 44)]
+    ws = dirty(max(trt.linear_xent_workspace_size(T, V, D), trt.linear_xent_bwd_workspace_size(T, V, D)))
+
+    def step(c):
+        loss, lse = trt.linear_xent(c.x, c.w, c.target, ignore_index=IGNORE, workspace=ws)
+        return (loss, lse) + trt.linear_xent_bwd(c.x, c.w, c.target, lse, c.dloss, ignore_index=IGNORE, workspace=ws)
+
+    want = [[t.clone() for t in step(c)] for c in cases]
+    side = torch.cuda.Stream()
+    graphs, outs = [], []
+    for c in cases:
+        with torch.cuda.stream(side):
+            step(c)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(step(c))
+        graphs.append(g)
+    for turn in range(6):
+        k = turn % 2
+        for t in outs[k]:
+            t.fill_(-1)
+        graphs[k].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs[k], want[k])), turn
