@@ -63,19 +63,27 @@ __device__ __forceinline__ void dma_one(__amdgpu_buffer_rsrc_t rs, uint32_t m0v,
 }
 
 // Swizzle of a k-contiguous stage, rows of 8 chunks: chunk (r, g) in slot
-// 8r + (g XOR sw(r)), sw(r) = r1 | r2 << 1 | (r0 XOR r3) << 2 in the bits of r.
-// Of one chunk, 8 consecutive rows fall on 8 distinct 16-byte groups of a
-// 128-byte window and 16 on 16 of a 256-byte one; rows 16 apart swizzle alike.
+// 8r + (g XOR sw(r)), sw(r) = r1 | (r1 XOR r2) << 1 | (r0 XOR r3) << 2 in the
+// bits of r; rows 16 apart swizzle alike.  A fragment read of 16 bytes a lane
+// passes 16 lanes at a time: of two neighbouring lane groups, rows 0-3 and 12-15
+// of one and 4-11 of the other (then the rest), and these read chunks that
+// differ in both low bits (frag_kchunk).  Their 16 words fall on 16 distinct
+// places of a 256-byte window.  (With r2 for r1 XOR r2 they met in pairs: four
+// cycles more for each read of eight.)
 TRT_HD int wide_swz(int r) {
-  return ((r >> 1) & 3) | (((r ^ (r >> 3)) & 1) << 2);
+  return ((r >> 1) & 1) | ((((r >> 1) ^ (r >> 2)) & 1) << 1) | (((r ^ (r >> 3)) & 1) << 2);
 }
 constexpr bool wide_swz_spreads() {
   for (int g = 0; g < 8; ++g)
-    for (int r0 = 0; r0 < 16; r0 += 8) {
-      int by8 = 0, by16 = 0;
-      for (int r = 0; r < 8; ++r) by8 |= 1 << ((g ^ wide_swz(r0 + r)) & 7);
-      for (int r = 0; r < 16; ++r) by16 |= 1 << ((r & 1) * 8 + (g ^ wide_swz(r)));
-      if (by8 != 0xFF || by16 != 0xFFFF || wide_swz(r0 + 16) != wide_swz(r0)) return false;
+    for (int first = 0; first < 2; ++first) {
+      int places = 0;
+      for (int r = 0; r < 16; ++r) {
+        const bool inner = r >= 4 && r < 12;
+        const int chunk = inner == (first != 0) ? g : g ^ 3;
+        places |= 1 << ((r & 1) * 8 + (chunk ^ wide_swz(r)));
+        if (wide_swz(r + 16) != wide_swz(r)) return false;
+      }
+      if (places != 0xFFFF) return false;
     }
   return true;
 }

@@ -28,7 +28,7 @@ constexpr Shape shape_of(int64_t chunks, bool backward) {
   if (chunks <= 768 && !backward) return {4, 3};
   if (chunks <= 1024) return {8, 2};
   if (!backward) return chunks <= 2048 ? Shape{16, 2} : Shape{16, 4};
-  return {8, chunks <= 2048 ? 4 : chunks <= 3072 ? 6 : 8};
+  return {8, chunks <= 4 * 512 ? 4 : chunks <= 6 * 512 ? 6 : 8};
 }
 static_assert(kNormMaxRowBytes / 16 == 16 * 64 * 4, "the longest row is one workgroup's");
 
