@@ -153,6 +153,13 @@ def test_long_rows_in_turns(cols, dtype):
     run_case(515, cols, dtype, torch.float32, seed=cols)
 
 
+@pytest.mark.parametrize("dtype,cols", [(torch.bfloat16, 1530), (torch.float16, 2047), (torch.bfloat16, 4090),
+                                        (torch.float16, 8184), (torch.float32, 765), (torch.float32, 1022)],
+                         ids=lambda v: NAMES.get(v, v))
+def test_large_workgroups_in_turns(cols, dtype):
+    run_case(4111, cols, dtype, torch.float32, seed=cols)
+
+
 @pytest.mark.parametrize("dtype", DTYPES, ids=NAMES.get)
 @pytest.mark.parametrize("rows", [1, 2, 3, 4, 31, 257, 4099])
 def test_row_counts(rows, dtype):

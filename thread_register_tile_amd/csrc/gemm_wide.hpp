@@ -24,6 +24,10 @@
 //     into set 0, with the copies of step kt + 2 into the free stage between
 //     the products.
 //
+// Bound by the matrix cores, and on large products by the power they may draw:
+// 8192 x 131072 x 4096 bf16 in 6.0 ms with the statistics' epilogue (1.46
+// PFLOP/s at 1.7 GHz), 6.55 on the pipelined kernel.
+//
 // An epilogue that leaves the stages alone (EPI::STREAMS) runs on a grid of one
 // workgroup per compute unit that walks the tiles: the copies of the next
 // tile's first two steps go out ahead of the epilogue, which covers their

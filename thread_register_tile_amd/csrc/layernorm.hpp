@@ -10,7 +10,9 @@
 // backward pass reads x and dy and writes dx once; a row lives in registers
 // from its load to its store, so the several sums over it cost no traffic.
 // The backward pass therefore takes no saved statistics: it forms them again
-// from the row it has to read anyway.
+// from the row it has to read anyway.  Measured on 16384 rows of 8192 bf16
+// elements: 91 us forward (5.9 TB/s), 151 backward (5.3 TB/s); a large copy
+// reaches 5.2, a streaming read 6.4.
 //
 // Cooperation: a row is cut into 16-byte chunks, chunk c going to lane
 // c mod 64W of the row's W waves, iteration c div 64W ("My Triton From
@@ -213,7 +215,7 @@ __global__ __launch_bounds__(NormShape<W>::THREADS) void layernorm_kernel(NormAr
 // them to its slice of `part` at the end, and norm_params_kernel adds the
 // slices in order.  The grid is fixed by the sizes (norm_grid), so the sums'
 // order is too: the results repeat bit for bit.
-// A workgroup is 16 waves, 16 / W rows at a time, and there is one to a
+// A workgroup is 16 or 8 waves, a row to each W of them, and there is one to a
 // compute unit: the fewer slices, the fewer bytes beside the rows' own (with
 // workgroups of one row, two to a unit, the slices were 8 % of the traffic of
 // 16384 rows of 8192, and 8 % of the time).

@@ -100,7 +100,7 @@ trt_status trt_linear_xent(int64_t tokens, int64_t vocab, int64_t width, const v
   trt::XentStatsArgs a{};
   const bool vec = width % 8 == 0 && ldx % 8 == 0 && ldw % 8 == 0 && aligned16(x) && aligned16(w);
   // (of more entries the stream's launch would have 2^32 threads)
-  const bool stream_w = vec && tokens <= trt::kXentStreamTokens && vocab <= trt::kMaxDim / 2;
+  const bool stream_w = vec && tokens <= trt::kXentStreamTokens && vocab <= trt::kMaxDim / 4;
   const int64_t chunk = kExtent / (2 * ldw) / 256 * 256;
   const bool pipelined = vec && chunk >= 256 && ((tokens - 1) * ldx + width) * 2 < kExtent;
   const int64_t step = pipelined && !stream_w ? chunk : vocab;
