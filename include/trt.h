@@ -527,8 +527,8 @@ trt_status trt_block_reduce(const void* x, int64_t n, int64_t block, int32_t dty
  * Errors before any HIP call: TRT_ERR_SIZE (rows or cols outside [1, 2^30], an
  * extent that overflows, a short workspace), TRT_ERR_STRIDE, TRT_ERR_NULL,
  * TRT_ERR_ALIGN, TRT_ERR_OVERLAP, TRT_ERR_DTYPE, TRT_ERR_UNSUPPORTED,
- * TRT_ERR_ARG; TRT_ERR_HIP if a launch fails.  Enqueued on `stream` (one kernel forward,
- * one or two backward).
+ * TRT_ERR_ARG; TRT_ERR_HIP if a launch fails.  Enqueued on `stream` (one
+ * kernel forward, one or two backward).
  */
 trt_status trt_layernorm(int64_t rows, int64_t cols, const void* x, int64_t ldx,
                          const void* gamma, const void* beta, float eps,
@@ -559,10 +559,10 @@ trt_status trt_layernorm_bwd(int64_t rows, int64_t cols, const void* dy, int64_t
  *
  * Tokens whose target equals ignore_index take part in nothing: loss = lse =
  * 0, a zero row in dx, no share of dw, whatever their row of x holds; they
- * cost next to no time either.  So do, in the backward pass, tokens
- * whose dloss and dlse are both zero.  A target outside [0, vocab) that
- * is not ignore_index gives loss = NaN (lse is the true one) and, in the
- * backward pass, a row of NaN in dx and NaN in dw: it is not read out of range.
+ * cost next to no time either.  The same goes, in the backward pass, for tokens
+ * whose dloss and dlse are both zero.  A target outside [0, vocab) that is not
+ * ignore_index gives loss = NaN (lse is the true one) and, in the backward
+ * pass, a row of NaN in dx and NaN in dw: nothing is read out of range for it.
  * A NaN or a positive infinity among a live token's logits makes its loss
  * NaN; a logit of -infinity has probability zero.
  *
@@ -574,11 +574,11 @@ trt_status trt_layernorm_bwd(int64_t rows, int64_t cols, const void* dy, int64_t
  * the forward pass's.  Logits, statistics and all sums are binary32.  The
  * backward pass works through the vocabulary in pieces of `piece` entries
  * (0: the library's choice; else a multiple of 64 up to 2^20, TRT_ERR_ARG
- * otherwise) and rounds g over the largest of the tokens' weights max(|dloss|,
- * |dloss + dlse|) once to in_dtype (for up to 64 tokens it keeps what that rounding leaves
- * in a second number).  In binary16 that loses bits of a g below 2^-28 of
- * that weight.
- * Results repeat bit for bit.
+ * otherwise) and rounds g over the largest finite one of the tokens' weights
+ * max(|dloss|, |dloss + dlse|) once to in_dtype (for up to 64 tokens it keeps
+ * what that rounding leaves in a second number).  In binary16 that loses bits
+ * of a g below 2^-28 of that weight.  A token whose weight is not finite
+ * spoils its own row of dx, and dw.  Results repeat bit for bit.
  *
  * workspace: device memory of at least trt_linear_xent_workspace_size(tokens,
  * vocab, width) or trt_linear_xent_bwd_workspace_size(tokens, vocab, width,
@@ -591,10 +591,11 @@ trt_status trt_layernorm_bwd(int64_t rows, int64_t cols, const void* dy, int64_t
  * and w with width, ldx and ldw multiples of 8 take the fast kernels.  No
  * output and no workspace may overlap any other buffer (TRT_ERR_OVERLAP).
  * 1 <= tokens <= 2^23, 1 <= vocab <= 2^30, 1 <= width <= 2^20, and any two of
- * them give fewer than 2^24 tiles of 128x128 (TRT_ERR_SIZE).  Errors before any HIP call: TRT_ERR_SIZE,
- * TRT_ERR_STRIDE, TRT_ERR_NULL, TRT_ERR_ALIGN, TRT_ERR_OVERLAP,
- * TRT_ERR_DTYPE, TRT_ERR_ARG; TRT_ERR_HIP if a launch fails.  Enqueued on
- * `stream`: two or three kernels forward; backward three, and up to three for each piece.
+ * them give fewer than 2^24 tiles of 128x128 (TRT_ERR_SIZE).  Errors before
+ * any HIP call: TRT_ERR_SIZE, TRT_ERR_STRIDE, TRT_ERR_NULL, TRT_ERR_ALIGN,
+ * TRT_ERR_OVERLAP, TRT_ERR_DTYPE, TRT_ERR_ARG; TRT_ERR_HIP if a launch fails.
+ * Enqueued on `stream`: two or three kernels forward (a product for each 2 GiB
+ * of w); backward three, and up to three for each piece.
  */
 int64_t trt_linear_xent_workspace_size(int64_t tokens, int64_t vocab, int64_t width);
 trt_status trt_linear_xent(int64_t tokens, int64_t vocab, int64_t width,
