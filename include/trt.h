@@ -575,9 +575,11 @@ trt_status trt_layernorm_bwd(int64_t rows, int64_t cols, const void* dy, int64_t
  * backward pass works through the vocabulary in pieces of `piece` entries
  * (0: the library's choice; else a multiple of 64 up to 2^20, TRT_ERR_ARG
  * otherwise) and rounds g over the largest finite one of the tokens' weights
- * max(|dloss|, |dloss + dlse|) once to in_dtype (for up to 64 tokens it keeps
- * what that rounding leaves in a second number).  In binary16 that loses bits
- * of a g below 2^-28 of that weight.  A token whose weight is not finite
+ * max(|dloss|, |dloss + dlse|) once to in_dtype.  For up to 64 tokens it keeps
+ * what that rounding leaves in a second number; for more, dx and dw carry its
+ * error beside their own rounding's, binary32 ones too: each g is off by at most
+ * half a step of in_dtype.  In binary16 g loses bits below 2^-28 of that
+ * weight.  A token whose weight is not finite
  * spoils its own row of dx, and dw.  Results repeat bit for bit.
  *
  * workspace: device memory of at least trt_linear_xent_workspace_size(tokens,
