@@ -579,8 +579,8 @@ trt_status trt_layernorm_bwd(int64_t rows, int64_t cols, const void* dy, int64_t
  * what that rounding leaves in a second number; for more, dx and dw carry its
  * error beside their own rounding's, binary32 ones too: each g is off by at most
  * half a step of in_dtype.  In binary16 g loses bits below 2^-28 of that
- * weight.  A token whose weight is not finite
- * spoils its own row of dx, and dw.  Results repeat bit for bit.
+ * weight.  A token whose dloss or dloss + dlse is
+ * not finite spoils its own row of dx, and dw.  Results repeat bit for bit.
  *
  * workspace: device memory of at least trt_linear_xent_workspace_size(tokens,
  * vocab, width) or trt_linear_xent_bwd_workspace_size(tokens, vocab, width,

@@ -15,10 +15,12 @@ namespace trt {
 // largest finite s_t.  Forward, it writes the ignored tokens' results.
 constexpr int kPrepThreads = 1024, kPrepEach = 8;
 
+// s_t: zero for a token without weight, NaN if either gradient is (the maximum
+// of a number and NaN would be the number; NaN in dl is in both as well).
 __device__ __forceinline__ float xent_weight(const XentPrepArgs& a, int64_t t, float& dl, float& both) {
   dl = a.dloss[t * a.inc_dloss];
   both = a.dlse ? dl + a.dlse[t * a.inc_dlse] : dl;
-  return __builtin_fmaxf(__builtin_fabsf(dl), __builtin_fabsf(both));
+  return both == both ? __builtin_fmaxf(__builtin_fabsf(dl), __builtin_fabsf(both)) : both;
 }
 
 // (BACKWARD as a template argument, so that the loads of a thread's tokens are
