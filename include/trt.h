@@ -504,7 +504,9 @@ trt_status trt_block_reduce(const void* x, int64_t n, int64_t block, int32_t dty
  *
  * All sums are binary32 (two rounds over the row, the mean corrected in the
  * second), each result is rounded once to its own type, and results repeat
- * bit for bit.  The backward pass forms mu and v again from x, so the forward
+ * bit for bit.  A row whose squared deviations sum to 2^128 or more, beyond
+ * binary32, has no norm: its h is 0, or NaN where the mean's correction
+ * overflows too.  The backward pass forms mu and v again from x, so the forward
  * pass keeps nothing for it.
  *
  * x, y, dy, dx: rows of dtype (TRT_F16, TRT_BF16 or TRT_F32) with leading

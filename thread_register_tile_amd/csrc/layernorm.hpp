@@ -85,6 +85,14 @@ __device__ __forceinline__ float rounded(float x) {
   return x;
 }
 
+// 1 / sqrt(v + eps), where rounding may leave v a little below zero.  NaN stays
+// NaN: v is infinity less infinity where the squares of the deviations and of the
+// mean's correction are beyond binary32, and no finite value may come of that
+// (the maximum of v and 0 would be 0).
+__device__ __forceinline__ float norm_rstd(float v, float eps) {
+  return 1.f / sqrtf((v < 0.f ? 0.f : v) + eps);
+}
+
 // Sum over the wave's 64 lanes, the same bits in every lane: within the quads,
 // eights and rows of 16 by data-parallel moves, then across the four rows.
 __device__ __forceinline__ float wave_sum(float v) {
@@ -193,7 +201,7 @@ __global__ __launch_bounds__(NormShape<W>::THREADS) void layernorm_kernel(NormAr
     row_sums<W, 2>(q, buf, turn, wave, W * grp);
     keep_packed(x);
     const float dbar = q[0] * inv;
-    const float rstd = 1.f / sqrtf(fmaxf(q[1] * inv - dbar * dbar, 0.f) + a.eps);
+    const float rstd = norm_rstd(q[1] * inv - dbar * dbar, a.eps);
     char* p = static_cast<char*>(a.out) + r * a.ldo * (int64_t)sizeof(typename C::Elem);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -328,7 +336,7 @@ __global__ __launch_bounds__(64 * WAVES) void layernorm_bwd_kernel(NormArgs a) {
     keep_packed(x);
     keep_packed(y);
     const float dbar = q[0] * inv;
-    const float rstd = 1.f / sqrtf(fmaxf(q[1] * inv - dbar * dbar, 0.f) + a.eps);
+    const float rstd = norm_rstd(q[1] * inv - dbar * dbar, a.eps);
     const float c1 = q[2] * inv;
     const float c2 = rstd * (q[3] * inv - dbar * c1);   // mean(u h)
     if (!live) continue;
