@@ -591,8 +591,10 @@ def _device(first, **others):
 def _on(dev, status_of):
     """status_of(stream) with dev current (a launch goes to the current device)."""
     torch = _torch()
-    # (the handle itself: making a Stream object of it takes 1.7 us of a call's 10)
-    stream = torch._C._cuda_getCurrentRawStream(dev.index) or None
+    # (the handle itself, where torch gives it: making a Stream object of it takes
+    # 1.7 us of a call's 10)
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    stream = (raw(dev.index) if raw else _stream(dev)) or None
     if torch.cuda.current_device() == dev.index:
         return _check(status_of(stream))
     with torch.cuda.device(dev):
