@@ -587,12 +587,16 @@ trt_status trt_layernorm_bwd(int64_t rows, int64_t cols, const void* dy, int64_t
  * workspace: device memory of at least trt_linear_xent_workspace_size(tokens,
  * vocab, width) or trt_linear_xent_bwd_workspace_size(tokens, vocab, width,
  * piece) bytes, 16-byte aligned, contents unspecified before and after; the
- * backward pass's holds one piece of g and dx's sums.  Calls that may overlap
+ * backward pass's holds one piece of g, a copy of x's rows and dx's sums (8192
+ * tokens x 131072 x 4096: 0.8 GiB in all).  Calls that may overlap
  * in time need a workspace each.  The size functions are host only and return
  * -1 on an argument error.
  *
  * Any strides and alignments to the element are allowed; 16-byte aligned x
- * and w with width, ldx and ldw multiples of 8 take the fast kernels.  No
+ * and w with width, ldx and ldw multiples of 8 take the fast kernels, as long as
+ * x spans less than 2 GiB less 8 KiB from its first row to its last (and, in the
+ * backward pass, so do its copy, g, and a piece's rows of w, which a smaller
+ * piece shortens; 256 rows of w in the forward pass).  Others take kernels that read element by element.  No
  * output and no workspace may overlap any other buffer (TRT_ERR_OVERLAP).
  * 1 <= tokens <= 2^23, 1 <= vocab <= 2^30, 1 <= width <= 2^20, and any two of
  * them give fewer than 2^24 tiles of 128x128 (TRT_ERR_SIZE).  Errors before

@@ -655,7 +655,8 @@ def layernorm(x, gamma=None, beta=None, *, eps=1e-5, out=None):
     float32, rows of unit inner stride; gamma and beta: one dtype, x's or
     float32.  out, if given, has x's shape and dtype and may not overlap the
     inputs; otherwise a new tensor is returned.  Runs on torch's current
-    stream; no synchronisation.
+    stream; no synchronisation, and nothing recorded for autograd: the result
+    never requires a gradient.
     """
     rows, cols, ldx = _rows(x, "x")
     param = next((t.dtype for t in (gamma, beta) if t is not None), x.dtype)
@@ -783,7 +784,8 @@ def linear_xent(x, w, target, *, ignore_index=-100, loss=None, lse=None, workspa
     Tokens whose target is ignore_index have loss and lse 0.  loss, lse and
     workspace (a uint8 tensor of linear_xent_workspace_size(...) bytes) are
     written if given, else allocated.  Runs on torch's current stream; no
-    synchronisation.
+    synchronisation, and nothing recorded for autograd: the results never
+    require a gradient (linear_xent_bwd gives them).
     """
     tokens, vocab, width, ldx, ldw = _xent_inputs(x, w, target)
     workspace = _workspace(workspace, linear_xent_workspace_size(tokens, vocab, width), x)

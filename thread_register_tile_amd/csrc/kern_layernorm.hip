@@ -41,9 +41,9 @@ int grid_of(int64_t rows, int groups, int most) {
 }
 
 // Forward workgroups to a compute unit, 16 waves in all (measured on 16384
-// rows of 8192 16-bit elements: 94 us, against 107 with twice as many), but
-// for one-wave rows, whose short loads want 32 (65536 rows of 512: 25.7 us
-// against 28.5).  Backward: one of 16 waves.
+// rows of 8192 16-bit elements: 93 us, against 106 with twice as many), but
+// for one-wave rows, whose short loads want 32 (65536 rows of 512: 26.7 us,
+// against 28.7 with 16).  Backward: one, of 16 or 8 waves (kBwdWaves).
 template <int W>
 constexpr int forward_most() { return W == 1 ? 8 : 16 / W; }
 

@@ -221,7 +221,7 @@ __global__ __launch_bounds__(NormShape<W>::THREADS) void layernorm_kernel(NormAr
 // sum(u)).  Every lane keeps the partial sums of dgamma and dbeta of its own
 // columns in registers over all its rows, in row order; the workgroup writes
 // them to its slice of `part` at the end, and norm_params_kernel adds the
-// slices in order.  The grid is fixed by the sizes (norm_grid), so the sums'
+// slices in order.  The grid is fixed by the sizes (norm_slices), so the sums'
 // order is too: the results repeat bit for bit.
 // A workgroup is 16 or 8 waves, a row to each W of them, and there is one to a
 // compute unit: the fewer slices, the fewer bytes beside the rows' own (with

@@ -113,10 +113,13 @@ struct XentBwdPlan {
   int64_t bytes;
 };
 
-// The piece the library chooses: G of at most 2^28 elements (512 MiB), but
-// 8192 entries at least, so that adding dX's sums (8 bytes per token, width
-// and piece) stays small beside the piece's products; neither G nor the
-// piece's rows of W are ever 2 GiB or more.
+// The piece the library chooses: G of at most 2^28 elements (512 MiB: up to
+// 32768 tokens), but 8192 entries at least, so that adding dX's sums (8 bytes per
+// token, width and piece) stays small beside the piece's products; and no more
+// than leaves G and as many rows of `width` below 2 GiB, the copies' limit, which
+// 256 entries keep up to 2^22 - 256 tokens.  (W's rows count as ldw long against
+// that limit: trt_xent.hip.)  X' and dX's sums take room beside G: 65536 tokens of
+// width 4096 over 131072 entries 512 MiB and 1 GiB, G another.
 constexpr int64_t xent_piece(int64_t tokens, int64_t vocab, int64_t width) {
   int64_t most = (int64_t(1) << 28) / tokens;
   if (most < 8192) most = 8192;
