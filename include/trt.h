@@ -581,8 +581,8 @@ trt_status trt_layernorm_bwd(int64_t rows, int64_t cols, const void* dy, int64_t
  * what that rounding leaves in a second number; for more, dx and dw carry its
  * error beside their own rounding's, binary32 ones too: each g is off by at most
  * half a step of in_dtype.  In binary16 g loses bits below 2^-28 of that
- * weight.  A token whose dloss or dloss + dlse is
- * not finite spoils its own row of dx, and dw.  Results repeat bit for bit.
+ * weight.  A token whose dloss or dloss + dlse is not finite spoils its own
+ * row of dx, and dw.  Results repeat bit for bit.
  *
  * workspace: device memory of at least trt_linear_xent_workspace_size(tokens,
  * vocab, width) or trt_linear_xent_bwd_workspace_size(tokens, vocab, width,
@@ -594,10 +594,11 @@ trt_status trt_layernorm_bwd(int64_t rows, int64_t cols, const void* dy, int64_t
  *
  * Any strides and alignments to the element are allowed; 16-byte aligned x
  * and w with width, ldx and ldw multiples of 8 take the fast kernels, as long as
- * x spans less than 2 GiB less 8 KiB from its first row to its last (and, in the
- * backward pass, so do its copy, g, and a piece's rows of w, which a smaller
- * piece shortens; 256 rows of w in the forward pass).  Others take kernels that read element by element.  No
- * output and no workspace may overlap any other buffer (TRT_ERR_OVERLAP).
+ * x spans less than 2 GiB less 8 KiB from its first row to its last, and so do
+ * 256 rows of w in the forward pass, x's copy, g and a piece's rows of w (which
+ * a smaller piece shortens) in the backward pass.  Others take kernels that
+ * read element by element.  No output and no workspace may overlap any other
+ * buffer (TRT_ERR_OVERLAP).
  * 1 <= tokens <= 2^23, 1 <= vocab <= 2^30, 1 <= width <= 2^20, and any two of
  * them give fewer than 2^24 tiles of 128x128 (TRT_ERR_SIZE).  Errors before
  * any HIP call: TRT_ERR_SIZE, TRT_ERR_STRIDE, TRT_ERR_NULL, TRT_ERR_ALIGN,

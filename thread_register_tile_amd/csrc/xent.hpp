@@ -30,10 +30,10 @@
 // binary32, |g| <= 2, and under a mean or a sum the entry that dominates a row,
 // p_target - 1, loses nothing where p_target is small.  A gradient sums terms of
 // either sign, so the terms' rounding errors stay one rounding's size against it
-// however many they are: bf16 gradients are off by 2.2e-3 of their norm for 77
-// tokens (16384 x 1024) and 1.9e-3 for 8192 (131072 x 4096), where a binary32 G
-// would leave 1.7e-3, their own rounding; binary16's results below 2^-14 weigh
-// more than G there (1.2e-3 either way for 4097 tokens, 32003 x 2560).  Without
+// however many they are: bf16 gradients are off by 2.2e-3 to 2.4e-3 of their
+// norm for 77 tokens (16384 x 1024) and 1.9e-3 for 8192 (131072 x 4096), where a
+// binary32 G would leave 1.7e-3, their own rounding; with binary16 the results'
+// loss below 2^-14 weighs more (1.2e-3 either way for 4097 tokens, 32003 x 2560).  Without
 // that rounding dX's and dW's products would be twice as long.  For few tokens,
 // where they wait for memory, they may be: G is held as two rows of 16-bit
 // numbers, the rounded value and what the rounding left, which is off by half a
