@@ -29,7 +29,7 @@
 extern "C" {
 #endif
 
-#define TRT_ABI_VERSION 14
+#define TRT_ABI_VERSION 15
 
 /* Status codes.  Every entry point returns one of these. */
 typedef enum {
@@ -622,6 +622,67 @@ trt_status trt_linear_xent_bwd(int64_t tokens, int64_t vocab, int64_t width,
                                void* dx, int64_t lddx, void* dw, int64_t lddw,
                                int32_t in_dtype, int32_t out_dtype, int64_t piece,
                                void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * Activations saved in 8 bits for the backward pass, and a linear layer's
+ * weight gradient from its saved input.  No page defines them; they are what a
+ * training step keeps for, and hands to, the library's products and norms.
+ *
+ * Of every 32 columns of a row (the last block may be shorter) scale holds one
+ * byte X and q an integer for each element, which stands for q * 2^(X - 133):
+ * the MX format's 8-bit integers with 8-bit exponents.
+ *
+ *   trt_act8_pack:    X = floor(log2(largest |x| of the block)) + 127, at least
+ *                     7; q = x / 2^(X - 133), rounded to nearest, ties to even,
+ *                     and held to [-127, 127].  A block that holds an infinity or
+ *                     a NaN has X = 255 and q = 0.
+ *   trt_act8_unpack:  x = q * 2^(X - 133), rounded to dtype; NaN where X = 255.
+ *                     Any bytes may be given (q = -128 and X < 7 too).
+ *   trt_act8_weight_grad:  dw = dy^T . x, x as trt_act8_unpack gives it in
+ *                     in_dtype, the sum over the tokens.
+ *
+ * An element is off by at most 2^-7 of the largest power of two in its block's
+ * largest magnitude (half that where it does not round up to 128 steps), or by
+ * 2^-127 where that is more.  Unpacking is exact in bf16 and binary32 for what
+ * trt_act8_pack made, and in binary16 where x was binary16.
+ *
+ * x: rows x cols of dtype (TRT_F16, TRT_BF16 or TRT_F32); q: rows x cols bytes;
+ * scale: rows x ceil(cols / 32) bytes.  dy: [tokens, outputs] of in_dtype
+ * (TRT_F16 or TRT_BF16); q, scale: the [tokens, inputs] input's; dw: [outputs,
+ * inputs] of out_dtype (TRT_F16, TRT_BF16 or TRT_F32), rounded once from
+ * binary32 sums.  Leading dimensions in elements: inputs >= 1, outputs >= their
+ * columns.  Any alignment to the element is allowed; no output and no workspace
+ * may overlap any other buffer (TRT_ERR_OVERLAP).  Results repeat bit for bit.
+ * A NaN or an infinity in dy spoils its output's row of dw; a token's block of
+ * NaN spoils 32 columns of it.
+ *
+ * workspace: device memory of at least trt_act8_weight_grad_workspace_size(...)
+ * bytes, 16-byte aligned, contents unspecified before and after: x restored to
+ * 16 bits, a copy of dy unless its address, lddy and outputs are multiples of 16
+ * bytes (outputs <= lddy <= 2^21), and where outputs x inputs give few tiles binary32 results of
+ * slices of the tokens.  dy is not read for the size: its address alone decides.
+ * Calls that may overlap in time need a workspace each.  The function is host
+ * only and returns -1 on an argument error.
+ *
+ * rows, cols in [1, 2^30]; tokens <= 2^23, outputs and inputs <= 2^20; fewer
+ * than 2^34 chunks of 16 bytes and than 2^24 output tiles (TRT_ERR_SIZE).
+ * Errors before any HIP call: TRT_ERR_SIZE, TRT_ERR_STRIDE, TRT_ERR_NULL,
+ * TRT_ERR_ALIGN, TRT_ERR_OVERLAP, TRT_ERR_DTYPE; TRT_ERR_HIP if a launch fails.
+ * Enqueued on `stream`: one kernel, the weight gradient two or three.
+ */
+trt_status trt_act8_pack(int64_t rows, int64_t cols, const void* x, int64_t ldx,
+                         int8_t* q, int64_t ldq, uint8_t* scale, int64_t lds,
+                         int32_t dtype, void* stream);
+trt_status trt_act8_unpack(int64_t rows, int64_t cols, const int8_t* q, int64_t ldq,
+                           const uint8_t* scale, int64_t lds, void* x, int64_t ldx,
+                           int32_t dtype, void* stream);
+int64_t trt_act8_weight_grad_workspace_size(int64_t tokens, int64_t outputs, int64_t inputs,
+                                            const void* dy, int64_t lddy);
+trt_status trt_act8_weight_grad(int64_t tokens, int64_t outputs, int64_t inputs,
+                                const void* dy, int64_t lddy, const int8_t* q, int64_t ldq,
+                                const uint8_t* scale, int64_t lds, void* dw, int64_t lddw,
+                                int32_t in_dtype, int32_t out_dtype, void* workspace,
+                                int64_t workspace_bytes, void* stream);
 
 /*
  * trt_abi_version -- the ABI version of the loaded library (TRT_ABI_VERSION

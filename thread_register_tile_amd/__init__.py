@@ -151,6 +151,15 @@ def lib():
         L.trt_linear_xent_bwd.argtypes = [i64, i64, i64, vp, i64, vp, i64, vp, i64, vp, vp, i64, vp,
                                           i64, vp, i64, vp, i64, i32, i32, i64, vp, i64, vp]
         L.trt_linear_xent_bwd.restype = i32
+        L.trt_act8_pack.argtypes = [i64, i64, vp, i64, vp, i64, vp, i64, i32, vp]
+        L.trt_act8_pack.restype = i32
+        L.trt_act8_unpack.argtypes = [i64, i64, vp, i64, vp, i64, vp, i64, i32, vp]
+        L.trt_act8_unpack.restype = i32
+        L.trt_act8_weight_grad_workspace_size.argtypes = [i64, i64, i64, vp, i64]
+        L.trt_act8_weight_grad_workspace_size.restype = i64
+        L.trt_act8_weight_grad.argtypes = [i64, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, i32,
+                                           i32, vp, i64, vp]
+        L.trt_act8_weight_grad.restype = i32
         L.trt_abi_version.argtypes = []
         L.trt_abi_version.restype = i32
         L.trt_last_error.argtypes = []
@@ -846,3 +855,97 @@ def linear_xent_bwd(x, w, target, lse, dloss, dlse=None, *, ignore_index=-100, n
         None if dw is None else dw.data_ptr(), lddw, _dtype_code(x), _dtype_code(out), piece,
         workspace.data_ptr(), workspace.nbytes, s))
     return dx, dw
+
+
+# ---- activations saved in 8 bits, and a weight gradient from them --------------------
+
+ACT8_BLOCK = 32     # columns to a scale
+
+
+def _act8(q, scale, name=""):
+    """(rows, cols, ldq, lds) of 8-bit rows and their scales."""
+    torch = _torch()
+    if q.dtype != torch.int8 or scale.dtype != torch.uint8:
+        raise TrtError(ERR_DTYPE, f"{name}q must be int8 and {name}scale uint8")
+    rows, cols, ldq = _rows(q, f"{name}q")
+    blocks = -(-cols // ACT8_BLOCK)
+    if scale.dim() != q.dim() or scale.shape[:-1] != q.shape[:-1] or scale.size(-1) != blocks:
+        raise TrtError(ERR_SIZE, f"{name}scale must be {[*q.shape[:-1], blocks]}")
+    return rows, cols, ldq, _rows(scale, f"{name}scale")[2]
+
+
+def act8_pack(x, *, q=None, scale=None):
+    """x's rows (its last dimension) in 8 bits: (q, scale), by trt_act8_pack.
+    x: float16, bfloat16 or float32, rows of unit inner stride; q: int8 of x's
+    shape; scale: uint8 of x's leading shape, one for every ACT8_BLOCK columns.
+    An element stands for q * 2^(scale - 133); a block that holds an infinity
+    or a NaN is NaN throughout.  q and scale are written if given, else
+    allocated.  Runs on torch's current stream; no synchronisation.
+    """
+    torch = _torch()
+    rows, cols, ldx = _rows(x, "x")
+    if q is None:
+        q = torch.empty_like(x, dtype=torch.int8, memory_format=torch.contiguous_format)
+    elif q.shape != x.shape:
+        raise TrtError(ERR_SIZE, f"q must be {list(x.shape)}")
+    if scale is None:
+        scale = x.new_empty((*x.shape[:-1], -(-cols // ACT8_BLOCK)), dtype=torch.uint8)
+    _, _, ldq, lds = _act8(q, scale)
+    dev = _device(x, q=q, scale=scale)
+    _on(dev, lambda s: lib().trt_act8_pack(rows, cols, x.data_ptr(), ldx, q.data_ptr(), ldq, scale.data_ptr(), lds,
+                                           _dtype_code(x), s))
+    return q, scale
+
+
+def act8_unpack(q, scale, dtype, *, out=None):
+    """What act8_pack's rows stand for, rounded to dtype (exact in bfloat16 and
+    float32, and in float16 for rows that were float16): trt_act8_unpack.  out,
+    if given, has q's shape and dtype; otherwise a new tensor is returned.  Runs
+    on torch's current stream; no synchronisation.
+    """
+    torch = _torch()
+    rows, cols, ldq, lds = _act8(q, scale)
+    if out is None:
+        out = torch.empty_like(q, dtype=dtype, memory_format=torch.contiguous_format)
+    elif out.shape != q.shape or out.dtype != dtype:
+        raise TrtError(ERR_SIZE, f"out must be {list(q.shape)} of {dtype}")
+    ldx = _rows(out, "out")[2]
+    dev = _device(q, scale=scale, out=out)
+    _on(dev, lambda s: lib().trt_act8_unpack(rows, cols, q.data_ptr(), ldq, scale.data_ptr(), lds, out.data_ptr(),
+                                             ldx, _dtype_code(out), s))
+    return out
+
+
+def act8_weight_grad_workspace_size(tokens, outputs, inputs, dy_ptr=0, lddy=None) -> int:
+    """trt_act8_weight_grad_workspace_size: bytes of workspace for a dy at
+    address dy_ptr with rows lddy elements apart (contiguous where None)."""
+    n = lib().trt_act8_weight_grad_workspace_size(tokens, outputs, inputs, dy_ptr or None,
+                                                  outputs if lddy is None else lddy)
+    if n < 0:
+        raise TrtError(ERR_ARG, last_error())
+    return n
+
+
+def act8_weight_grad(dy, q, scale, *, out_dtype=None, dw=None, workspace=None):
+    """The weight gradient dy.T @ x of a linear layer whose input x [..., inputs]
+    was saved by act8_pack: trt_act8_weight_grad.  dy: [..., outputs], float16 or
+    bfloat16, q's leading shape; dw: [outputs, inputs] of out_dtype (default:
+    dy's, or that of the dw given).  dw and workspace (a uint8 tensor of
+    act8_weight_grad_workspace_size(...) bytes) are written if given, else
+    allocated.  Runs on torch's current stream; no synchronisation.
+    """
+    tokens, inputs, ldq, lds = _act8(q, scale)
+    rows, outputs, lddy = _rows(dy, "dy")
+    if dy.shape[:-1] != q.shape[:-1]:
+        raise TrtError(ERR_SIZE, f"dy must have q's leading shape {list(q.shape[:-1])}")
+    if dw is None:
+        dw = dy.new_empty((outputs, inputs), dtype=out_dtype or dy.dtype)
+    elif dw.dim() != 2 or dw.shape != (outputs, inputs) or dw.dtype != (out_dtype or dw.dtype):
+        raise TrtError(ERR_SIZE, f"dw must be [{outputs}, {inputs}] of {out_dtype or dw.dtype}")
+    lddw = _rows(dw, "dw")[2]
+    workspace = _workspace(workspace, act8_weight_grad_workspace_size(tokens, outputs, inputs, dy.data_ptr(), lddy), dy)
+    dev = _device(dy, q=q, scale=scale, dw=dw, workspace=workspace)
+    _on(dev, lambda s: lib().trt_act8_weight_grad(tokens, outputs, inputs, dy.data_ptr(), lddy, q.data_ptr(), ldq,
+                                                  scale.data_ptr(), lds, dw.data_ptr(), lddw, _dtype_code(dy),
+                                                  _dtype_code(dw), workspace.data_ptr(), workspace.nbytes, s))
+    return dw
