@@ -685,6 +685,97 @@ trt_status trt_act8_weight_grad(int64_t tokens, int64_t outputs, int64_t inputs,
                                 int64_t workspace_bytes, void* stream);
 
 /*
+ * What lies between two blocks of a residual model, in one pass over the rows,
+ * and its gradients.  No page defines it; it is the layer norm above, behind a
+ * block and in front of the next, fused with the block's gate and the residual
+ * stream.  With N(x) = (x - mu) / sqrt(mean((x - mu)^2) + eps), mu the row's
+ * mean, or 0 with rms:
+ *
+ *   trt_block_norm:      u     = N(y) * post_gamma + post_beta  (post; else u = y)
+ *                        r_out = alpha * r + gate * u
+ *                        h     = N(r_out) * gamma + beta
+ *   trt_block_norm_bwd:  for dh and dr_out, the gradients that reach h and r_out:
+ *                        t = dh * gamma;  e = dr_out + J_r^T t;  dr = alpha * e
+ *                        s = gate * post_gamma * e;  dy = J_y^T s  (post; else dy = s)
+ *                        dgate = sum of e * u,  dpost_gamma = sum of gate * e * N(y)
+ *                        dpost_beta = sum of gate * e
+ *                        dgamma = sum of dh * N(r_out),  dbeta = sum of dh
+ *
+ * with J^T v = (v - mean(v) - N mean(v N)) / sqrt(... + eps), without mean(v) under
+ * rms.  h comes of r_out before its rounding; the backward pass takes r_out and
+ * y as they are given and forms their norms again.  Sums are binary32 as the
+ * layer norm's, each result is rounded once, and results repeat bit for bit.  A
+ * row whose squares sum to 2^128 or more has no norm (h: 0 or NaN).
+ *
+ * r, y, r_out, h, dh, dr_out, dr, dy: rows x cols of dtype (TRT_F16, TRT_BF16 or
+ * TRT_F32), leading dimensions in elements: inputs >= 1, outputs >= cols.  h may be
+ * NULL (no norm follows); dh or dr_out may be NULL (zero), not both; without dh
+ * r_out is not read and may be NULL, and dgamma and dbeta are refused.  In the
+ * backward pass r_out and y may each be 8-bit rows of trt_act8_pack (scale not
+ * NULL), read as trt_act8_unpack gives them in dtype.
+ *
+ * gate: [ceil(rows / rows_per_gate), cols] of gate_dtype, row i of the block under
+ * gate row i / rows_per_gate: one gate for all rows, one for each sequence, one
+ * for each row.  NULL stands for ones.  post_gamma, post_beta, gamma, beta: [cols]
+ * of param_dtype; NULL stands for ones and zeros.  gate_dtype and param_dtype are
+ * dtype or TRT_F32.  The gradients have their operands' shapes and types; each
+ * may be NULL.  alpha, eps: finite, eps >= 0; post, rms: 0 or 1 (TRT_ERR_ARG, and
+ * for post_gamma, post_beta or their gradients without post).  Any alignment
+ * to the element is allowed.  A row holds at most 32768 bytes
+ * (TRT_ERR_UNSUPPORTED).  No output may overlap any other buffer
+ * (TRT_ERR_OVERLAP).  Elements past cols are neither read nor written.
+ *
+ * workspace (backward pass with a gradient of a parameter, or of a gate row that
+ * covers several rows; not touched otherwise): device memory of at least
+ * trt_block_norm_bwd_workspace_size(rows, cols, rows_per_gate, dtype) bytes
+ * (rows_per_gate 0: no gate), 16-byte aligned, contents unspecified before and
+ * after: four binary32 sums per column for each of up to 1024 workgroups, or for
+ * each gate row where there are more.  Host only, -1 on an argument error.  Calls
+ * that may overlap in time need a workspace each.
+ *
+ * Errors before any HIP call: TRT_ERR_SIZE (rows or cols outside [1, 2^30],
+ * 2^22 or more gate rows of several rows in the backward pass, an extent that
+ * overflows, a short workspace), TRT_ERR_STRIDE, TRT_ERR_NULL, TRT_ERR_ALIGN,
+ * TRT_ERR_OVERLAP, TRT_ERR_DTYPE, TRT_ERR_UNSUPPORTED, TRT_ERR_ARG; TRT_ERR_HIP if
+ * a launch fails.  Enqueued on `stream` (one kernel forward, one or two backward).
+ */
+typedef struct {
+  const void* gate;
+  int64_t ldg, rows_per_gate;
+  const void *post_gamma, *post_beta, *gamma, *beta;
+  float alpha, eps;
+  int32_t post, rms;
+  int32_t gate_dtype, param_dtype;
+} trt_block;
+
+/* Rows of dtype, or with scale not NULL the q of trt_act8_pack (ld in bytes). */
+typedef struct {
+  const void* x;
+  int64_t ld;
+  const uint8_t* scale;
+  int64_t lds;
+} trt_saved;
+
+typedef struct {
+  void* gate;
+  int64_t ldg;
+  void *post_gamma, *post_beta, *gamma, *beta;
+} trt_block_grads;
+
+trt_status trt_block_norm(int64_t rows, int64_t cols, const void* r, int64_t ldr,
+                          const void* y, int64_t ldy, const trt_block* block,
+                          void* r_out, int64_t ldro, void* h, int64_t ldh,
+                          int32_t dtype, void* stream);
+int64_t trt_block_norm_bwd_workspace_size(int64_t rows, int64_t cols, int64_t rows_per_gate,
+                                          int32_t dtype);
+trt_status trt_block_norm_bwd(int64_t rows, int64_t cols, const void* dh, int64_t lddh,
+                              const void* dr_out, int64_t lddro, const trt_saved* r_out,
+                              const trt_saved* y, const trt_block* block,
+                              void* dr, int64_t lddr, void* dy, int64_t lddy,
+                              const trt_block_grads* grads, int32_t dtype,
+                              void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
  * trt_abi_version -- the ABI version of the loaded library (TRT_ABI_VERSION
  * at build time).  "Named layouts", section "Runtime and compilation": the
  * launch ABI keeps versioned layout obligations so that caching and reload

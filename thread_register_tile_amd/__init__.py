@@ -57,6 +57,24 @@ class Epilogue(ctypes.Structure):
                 ("row_scale", ctypes.c_void_p)]
 
 
+class Block(ctypes.Structure):
+    _fields_ = [("gate", ctypes.c_void_p), ("ldg", ctypes.c_int64), ("rows_per_gate", ctypes.c_int64),
+                ("post_gamma", ctypes.c_void_p), ("post_beta", ctypes.c_void_p),
+                ("gamma", ctypes.c_void_p), ("beta", ctypes.c_void_p), ("alpha", ctypes.c_float),
+                ("eps", ctypes.c_float), ("post", ctypes.c_int32), ("rms", ctypes.c_int32),
+                ("gate_dtype", ctypes.c_int32), ("param_dtype", ctypes.c_int32)]
+
+
+class Saved(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("ld", ctypes.c_int64), ("scale", ctypes.c_void_p),
+                ("lds", ctypes.c_int64)]
+
+
+class BlockGrads(ctypes.Structure):
+    _fields_ = [("gate", ctypes.c_void_p), ("ldg", ctypes.c_int64), ("post_gamma", ctypes.c_void_p),
+                ("post_beta", ctypes.c_void_p), ("gamma", ctypes.c_void_p), ("beta", ctypes.c_void_p)]
+
+
 class TileDesc(ctypes.Structure):
     _fields_ = [("bm", ctypes.c_int32), ("bn", ctypes.c_int32), ("bk", ctypes.c_int32)]
 
@@ -160,6 +178,15 @@ def lib():
         L.trt_act8_weight_grad.argtypes = [i64, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, i32,
                                            i32, vp, i64, vp]
         L.trt_act8_weight_grad.restype = i32
+        L.trt_block_norm.argtypes = [i64, i64, vp, i64, vp, i64, ctypes.POINTER(Block), vp, i64, vp, i64,
+                                     i32, vp]
+        L.trt_block_norm.restype = i32
+        L.trt_block_norm_bwd_workspace_size.argtypes = [i64, i64, i64, i32]
+        L.trt_block_norm_bwd_workspace_size.restype = i64
+        L.trt_block_norm_bwd.argtypes = [i64, i64, vp, i64, vp, i64, ctypes.POINTER(Saved),
+                                         ctypes.POINTER(Saved), ctypes.POINTER(Block), vp, i64, vp, i64,
+                                         ctypes.POINTER(BlockGrads), i32, vp, i64, vp]
+        L.trt_block_norm_bwd.restype = i32
         L.trt_abi_version.argtypes = []
         L.trt_abi_version.restype = i32
         L.trt_last_error.argtypes = []
@@ -949,3 +976,169 @@ def act8_weight_grad(dy, q, scale, *, out_dtype=None, dw=None, workspace=None):
                                                   scale.data_ptr(), lds, dw.data_ptr(), lddw, _dtype_code(dy),
                                                   _dtype_code(dw), workspace.data_ptr(), workspace.nbytes, s))
     return dw
+
+
+# ---- the norms around a block with its gate and residual, and their gradients ---------
+
+def _gate_span(gate, shape, rows, cols, rows_per_gate):
+    """The rows that each row of a gate covers: the gate [cols] is for all rows;
+    one of x's leading sizes, from some point on 1 (and x's last), broadcasts
+    over what follows; with rows_per_gate it is [ceil(rows / that), cols]."""
+    if rows_per_gate is not None:
+        if rows_per_gate < 1 or gate.dim() != 2 or gate.shape != (-(-rows // rows_per_gate), cols):
+            raise TrtError(ERR_SIZE, f"gate must be [{-(-rows // max(rows_per_gate, 1))}, {cols}] for rows_per_gate {rows_per_gate}")
+        return rows_per_gate
+    if gate.dim() == 1 and gate.size(0) == cols:
+        return rows
+    span, at = 1, gate.dim() - 2
+    while at >= 0 and gate.size(at) == 1:
+        span *= shape[at] if gate.dim() == len(shape) else 1
+        at -= 1
+    if gate.dim() != len(shape) or gate.size(-1) != cols or gate.shape[:at + 1] != shape[:at + 1]:
+        raise TrtError(ERR_SIZE, f"gate {list(gate.shape)} does not cover rows of {list(shape)}: [{cols}], or leading "
+                                 "sizes followed by ones, or rows_per_gate given")
+    return span
+
+
+def _block(x, gate, post, post_gamma, post_beta, gamma, beta, alpha, rms, eps, rows_per_gate):
+    """(Block, gate's span or 0, parameters' dtype) for rows of x."""
+    rows, cols, _ = _rows(x, "x")
+    param = next((t.dtype for t in (post_gamma, post_beta, gamma, beta) if t is not None), x.dtype)
+    b = Block()
+    b.post_gamma, b.post_beta = _vector(post_gamma, "post_gamma", cols, param), _vector(post_beta, "post_beta", cols, param)
+    b.gamma, b.beta = _vector(gamma, "gamma", cols, param), _vector(beta, "beta", cols, param)
+    b.alpha, b.eps, b.post, b.rms = alpha, eps, int(post), int(rms)
+    b.param_dtype = _dtype_code(x) if param is x.dtype else _code_of(param)
+    span = 0
+    if gate is not None:
+        span = _gate_span(gate, x.shape, rows, cols, rows_per_gate)
+        b.gate, b.ldg, b.rows_per_gate, b.gate_dtype = gate.data_ptr(), _rows(gate, "gate")[2], span, _dtype_code(gate)
+    elif rows_per_gate is not None:
+        raise TrtError(ERR_ARG, "rows_per_gate without a gate")
+    return b, span, param
+
+
+def _code_of(dtype):
+    torch = _torch()
+    codes = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
+    if dtype not in codes:
+        raise TrtError(ERR_DTYPE, f"unsupported dtype {dtype}")
+    return codes[dtype]
+
+
+def block_norm(r, y, gate=None, *, post=True, post_gamma=None, post_beta=None, gamma=None, beta=None,
+               alpha=1.0, rms=False, eps=1e-5, rows_per_gate=None, need_h=True, r_out=None, h=None):
+    """The end of a block and the start of the next: (r_out, h) of
+        u = norm(y) * post_gamma + post_beta   (u = y without post)
+        r_out = alpha * r + gate * u
+        h = norm(r_out) * gamma + beta
+    by trt_block_norm.  r, the residual stream, and y, the block's output, have
+    one shape and dtype; the norms are layer norms, or root mean square norms
+    with rms.  gate (ones where None): [cols] for every row, y's shape, y's
+    leading sizes followed by ones ([batch, 1, cols] for [batch, tokens, cols]),
+    or [ceil(rows / rows_per_gate), cols] with rows_per_gate; y's dtype or
+    float32.  post_gamma, post_beta, gamma, beta: [cols] of one dtype, y's or
+    float32; ones and zeros where None.  Without need_h no norm follows and h is
+    None.  r_out and h are written if given, else allocated.  Runs on torch's
+    current stream; no synchronisation, and nothing recorded for autograd
+    (block_norm_bwd gives the gradients).
+    """
+    if y.shape != r.shape or y.dtype != r.dtype:
+        raise TrtError(ERR_SIZE, f"y must be {list(r.shape)} of {r.dtype}")
+    if h is not None and not need_h:
+        raise TrtError(ERR_ARG, "h given without need_h")
+    rows, cols, ldr = _rows(r, "r")
+    block, _, _ = _block(r, gate, post, post_gamma, post_beta, gamma, beta, alpha, rms, eps, rows_per_gate)
+    r_out = _like(r_out, r, "r_out")
+    if need_h:
+        h = _like(h, r, "h")
+    ldro, ldh = _rows(r_out, "r_out")[2], 0 if h is None else _rows(h, "h")[2]
+    dev = _device(r, y=y, gate=gate, post_gamma=post_gamma, post_beta=post_beta, gamma=gamma, beta=beta, r_out=r_out, h=h)
+    _on(dev, lambda s: lib().trt_block_norm(rows, cols, r.data_ptr(), ldr, y.data_ptr(), _rows(y, "y")[2], block,
+                                            r_out.data_ptr(), ldro, None if h is None else h.data_ptr(), ldh,
+                                            _dtype_code(r), s))
+    return r_out, h
+
+
+def block_norm_bwd_workspace_size(rows, cols, rows_per_gate=0, dtype=F16) -> int:
+    """trt_block_norm_bwd_workspace_size: bytes of workspace of the backward
+    pass (rows_per_gate 0: no gate)."""
+    n = lib().trt_block_norm_bwd_workspace_size(rows, cols, rows_per_gate, dtype)
+    if n < 0:
+        raise TrtError(ERR_ARG, last_error())
+    return n
+
+
+def _saved(t, name, shape, dtype):
+    """(Saved, its tensors) of rows of dtype, or of 8-bit ones as (q, scale)."""
+    if isinstance(t, (tuple, list)):
+        q, scale = t
+        _, _, ldq, lds = _act8(q, scale, f"{name}'s ")
+        if q.shape != shape:
+            raise TrtError(ERR_SIZE, f"{name}'s q must be {list(shape)}")
+        return Saved(q.data_ptr(), ldq, scale.data_ptr(), lds), {f"{name}'s q": q, f"{name}'s scale": scale}
+    if t.shape != shape or t.dtype != dtype:
+        raise TrtError(ERR_SIZE, f"{name} must be {list(shape)} of {dtype}, or act8_pack's (q, scale) of that shape")
+    return Saved(t.data_ptr(), _rows(t, name)[2], None, 0), {name: t}
+
+
+def block_norm_bwd(dh, dr_out, r_out, y, gate=None, *, post=True, post_gamma=None, post_beta=None, gamma=None,
+                   alpha=1.0, rms=False, eps=1e-5, rows_per_gate=None, params=True, dr=None, dy=None, workspace=None):
+    """The gradients of block_norm for dh and dr_out, those of its results:
+    (dr, dy, dgate, dpost_gamma, dpost_beta, dgamma, dbeta), by
+    trt_block_norm_bwd.  Either of dh and dr_out may be None (zero); r_out is
+    the forward pass's result, y its input, each a tensor or the (q, scale) of
+    act8_pack, read as act8_unpack gives them in dh's dtype; r_out may be None
+    without dh.  The other arguments are the forward pass's (the gradients do not
+    depend on beta).  dgate is None without a gate, dpost_gamma and dpost_beta
+    without post, dgamma and dbeta without dh, all five with params=False; they
+    have their operand's shape and dtype (the parameters' one dtype, float32
+    where none is given).  dr, dy and workspace (a uint8 tensor of
+    block_norm_bwd_workspace_size(...) bytes) are written if given, else
+    allocated.  Runs on torch's current stream; no synchronisation.
+    """
+    torch = _torch()
+    up = dr_out if dh is None else dh
+    if up is None:
+        raise TrtError(ERR_NULL, "dh or dr_out must be given")
+    rows, cols, _ = _rows(up, "dh")
+    if dr_out is not None and (dr_out.shape != up.shape or dr_out.dtype != up.dtype):
+        raise TrtError(ERR_SIZE, f"dr_out must be {list(up.shape)} of {up.dtype}")
+    if dh is not None and r_out is None:
+        raise TrtError(ERR_NULL, "dh needs r_out")
+    block, span, param = _block(up, gate, post, post_gamma, post_beta, gamma, None, alpha, rms, eps, rows_per_gate)
+    if gamma is None and post_gamma is None and post_beta is None:
+        param, block.param_dtype = torch.float32, F32
+    code = _dtype_code(up)
+    sy, tensors = _saved(y, "y", up.shape, up.dtype)
+    sr = None
+    if dh is not None:
+        sr, more = _saved(r_out, "r_out", up.shape, up.dtype)
+        tensors.update(more)
+    dr, dy = _like(dr, up, "dr"), _like(dy, up, "dy")
+    grads = BlockGrads()
+    dgate = dpg = dpb = dg = db = None
+    if params:
+        if gate is not None:
+            dgate = torch.empty_like(gate, memory_format=torch.contiguous_format)
+            grads.gate, grads.ldg = dgate.data_ptr(), cols
+        made = iter(up.new_empty((2 * post + 2 * (dh is not None), cols), dtype=param))
+        if post:
+            dpg, dpb = next(made), next(made)
+            grads.post_gamma, grads.post_beta = dpg.data_ptr(), dpb.data_ptr()
+        if dh is not None:
+            dg, db = next(made), next(made)
+            grads.gamma, grads.beta = dg.data_ptr(), db.data_ptr()
+        workspace = _workspace(workspace, block_norm_bwd_workspace_size(rows, cols, span, code), up)
+    else:
+        workspace = None
+    dev = _device(up, dr_out=dr_out, gate=gate, post_gamma=post_gamma, post_beta=post_beta, gamma=gamma, dr=dr, dy=dy,
+                  workspace=workspace, **tensors)
+    ws, wsb = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
+
+    def ptr(t, name):
+        return (None, 0) if t is None else (t.data_ptr(), _rows(t, name)[2])
+
+    _on(dev, lambda s: lib().trt_block_norm_bwd(rows, cols, *ptr(dh, "dh"), *ptr(dr_out, "dr_out"), sr, sy, block,
+                                                *ptr(dr, "dr"), *ptr(dy, "dy"), grads, code, ws, wsb, s))
+    return dr, dy, dgate, dpg, dpb, dg, db

@@ -1,0 +1,52 @@
+// kern_blocknorm.hip -- instances of the block norm's forward kernel and of the
+// kernel that adds the backward pass's sums, and the rules that pick the
+// shapes.
+#include "blocknorm.hpp"
+#include "blocknorm_shape.hpp"
+#include "blockparams.hpp"
+#include "launch.hpp"
+
+namespace trt {
+
+namespace {
+
+template <class F>
+hipError_t with_type(int dt, F&& f) {
+  if (dt == DT_F16) return f.template operator()<DT_F16>();
+  if (dt == DT_BF16) return f.template operator()<DT_BF16>();
+  return f.template operator()<DT_F32>();
+}
+
+}  // namespace
+
+BlockCut block_norm_cut(int64_t rows, int64_t cols, int64_t span, int dt) {
+  const int64_t groups = (rows + span - 1) / span;
+  return {groups, block_slices(rows, span, groups, block_chunks(cols, dt))};
+}
+
+hipError_t launch_block_norm(const BlockNormArgs& a, int dt, hipStream_t s) {
+  return with_type(dt, [&]<int DT>() {
+    return with_block_shape(block_chunks(a.cols, DT), [&]<int W, int K>() {
+      constexpr int THREADS = NormShape<W>::THREADS;
+      const int64_t need = (a.rows + NormShape<W>::GROUPS - 1) / NormShape<W>::GROUPS;
+      const dim3 grid(even_grid(need, forward_units<W>())), block(THREADS);
+      if (a.gate && a.span == 1) return launch(block_norm_kernel<DT, W, K, true>, grid, block, 0, s, a);
+      return launch(block_norm_kernel<DT, W, K, false>, grid, block, 0, s, a);
+    });
+  });
+}
+
+hipError_t launch_block_norm_bwd(const BlockNormArgs& a, const BlockParamsArgs& q, int dt, hipStream_t s) {
+  const int64_t groups = q.groups;
+  const hipError_t e = dt == DT_F16    ? launch_block_norm_rows<DT_F16>(a, groups, s)
+                       : dt == DT_BF16 ? launch_block_norm_rows<DT_BF16>(a, groups, s)
+                                       : launch_block_norm_rows<DT_F32>(a, groups, s);
+  if (e != hipSuccess || !a.part) return e;
+  // gate rows: a workgroup's 16 waves take one each, or share one of many slices
+  int64_t gates = 0;
+  if (q.dgate) gates = q.slices >= kBlockParamsWaves ? groups : (groups + kBlockParamsWaves - 1) / kBlockParamsWaves;
+  return launch(block_params_kernel, dim3((q.cols + 63) / 64, 4 + (gates < 4096 ? gates : 4096)),
+                dim3(64 * kBlockParamsWaves), 0, s, q);
+}
+
+}  // namespace trt
