@@ -49,24 +49,86 @@ __device__ __forceinline__ const void* row_of(const void* p, bool wide, int64_t 
   return static_cast<const char*>(p) + row * ld * (wide ? 4 : narrow);
 }
 
-// Sums of N values over the W waves of a row: row_sums with more values.
+// Sums of several values at once.  Each step that halves the lanes of one value's
+// sum takes two values into one register, so N values cost as many moves as two
+// or three alone: lanes 32 apart (permlane32_swap(x, y) leaves both halves of x in
+// the lower lanes and both of y in the upper), then 16, then 8; and four steps
+// within the lanes that are left.  Every step's order is fixed, so all waves have
+// the same bits.
+__device__ __forceinline__ float swap_add32(float x, float y) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(y), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ __forceinline__ float swap_add16(float x, float y) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(y), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float x) {
+  return x + __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), CTRL, 0xF, 0xF, true));
+}
+constexpr int kRowRor = 0x120;   // rotation within 16 lanes
+
+// Lanes 64 / N i .. 64 / N (i + 1) - 1 get the wave's sum of v[i]; N: 1, 2, 4 or 8.
+template <int N>
+__device__ __forceinline__ float wave_fold(const float (&v)[N]) {
+  static_assert(N == 1 || N == 2 || N == 4 || N == 8, "halves of the lanes");
+  float x;
+  if constexpr (N == 8) {
+    float h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = swap_add32(v[i], v[i + 4]);
+    const float a = swap_add16(h[0], h[2]), b = swap_add16(h[1], h[3]);
+    const float a8 = dpp_add<kRowRor + 8>(a), b8 = dpp_add<kRowRor + 8>(b);
+    x = threadIdx.x & 8 ? b8 : a8;
+  } else {
+    if constexpr (N == 4) x = swap_add16(swap_add32(v[0], v[2]), swap_add32(v[1], v[3]));
+    else if constexpr (N == 2) x = swap_add32(v[0], v[1]);
+    else x = swap_add32(v[0], v[0]);
+    if constexpr (N < 4) x = swap_add16(x, x);
+    x = dpp_add<kRowRor + 8>(x);
+  }
+  x = dpp_add<0x141>(x);    // mirror of 8 lanes
+  x = dpp_add<0x4E>(x);     // quad lanes 2 3 0 1
+  return dpp_add<0xB1>(x);  // quad lanes 1 0 3 2
+}
+
+__device__ __forceinline__ float lane_value(float x, int lane) {
+  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), lane));
+}
+
+// Sums of N values over the W waves of a row.  W > 1: the waves meet in LDS, in
+// the slots of `buf` from wave `first` on (two turns used alternately, so one
+// barrier a turn suffices: see row_sums).  Every wave of the workgroup calls it.
 template <int W, int N>
-__device__ __forceinline__ void meet(float (&v)[N], float (*buf)[16][8], int& turn, int wave, int first) {
+__device__ __forceinline__ void meet(float (&v)[N], float (*buf)[128], int& turn, int wave, int first) {
+  static_assert(W <= 16 && N <= 8, "one slot per wave and value");
+  constexpr int M = N <= 2 ? N : N <= 4 ? 4 : 8, EACH = 64 / M;
+  const int lane = threadIdx.x & 63;
+  float all[M];
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
-  if constexpr (W > 1) {
-    static_assert(W <= 16 && N <= 8, "one slot per wave and value");
-    if ((threadIdx.x & 63) == 0)
+  for (int i = 0; i < M; ++i) all[i] = i < N ? v[i] : 0.f;
+  float x = wave_fold<M>(all);
+  if constexpr (W == 1) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) buf[turn][first + wave][i] = v[i];
+    for (int i = 0; i < N; ++i) v[i] = lane_value(x, EACH * i);
+  } else {
+    if (lane % EACH == 0) buf[turn][(first + wave) * M + lane / EACH] = x;
     __syncthreads();
+    // lane l: value l mod M of wave l div M
+    const float* from = &buf[turn][first * M];
+    x = 0.f;
+    if (W * M >= 64 || lane < W * M) x = from[lane];
+    if constexpr (W * M > 64)
+      if (lane < W * M - 64) x += from[64 + lane];
+    if constexpr (M <= 8) x = dpp_add<kRowRor + 8>(x);
+    if constexpr (M <= 4) x = dpp_add<kRowRor + 4>(x);
+    if constexpr (M <= 2) x = dpp_add<kRowRor + 2>(x);
+    if constexpr (M <= 1) x = dpp_add<kRowRor + 1>(x);
+    x = swap_add16(x, x);
+    x = swap_add32(x, x);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      float s = buf[turn][first][i];
-#pragma unroll
-      for (int w = 1; w < W; ++w) s += buf[turn][first + w][i];
-      v[i] = s;
-    }
+    for (int i = 0; i < N; ++i) v[i] = lane_value(x, i);
     turn ^= 1;
   }
 }
@@ -79,7 +141,7 @@ __global__ __launch_bounds__(NormShape<W>::THREADS) void block_norm_kernel(Block
   using C = RowChunk<DT>;
   constexpr int VEC = C::VEC, LANES = 64 * W, GROUPS = NormShape<W>::GROUPS, E = sizeof(typename C::Elem);
   constexpr bool KEEP = W < 16;
-  __shared__ float buf[2][16][8];
+  __shared__ float buf[2][128];
   // the wave's index in a scalar register: row addresses are then scalar too
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wave = w % W, grp = w / W;
@@ -221,9 +283,11 @@ __global__ __launch_bounds__(NormShape<W>::THREADS) void block_norm_kernel(Block
 // The backward pass over the rows: workgroup `slice` of a gate row's `slices`
 // takes that row's rows in turn, GROUPS at a time.  Three rounds of sums: the
 // means of r' and y; the spreads, mean(t), mean(t rhat); mean(s), mean(s yhat).
+// RMS: without the means, two rounds of four and one (a third of the arithmetic,
+// which with 8-bit rows takes as long as the memory).
 // AHEAD: the next row is loaded ahead, KEPT: gamma and post_gamma stay in
 // registers, where the sums leave room for them.
-template <int DT, int W, int K, int WAVES>
+template <int DT, int W, int K, int WAVES, bool RMS>
 __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArgs a) {
   using C = RowChunk<DT>;
   using Q = Act8Chunk<DT>;
@@ -231,7 +295,7 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
   constexpr int ROOM = WAVES <= 8 ? 216 : 0;         // of 256 registers (168 and 128 of 12 and 16 waves)
   constexpr int HELD = K * (16 + 5 * VEC);           // the rows, e and the sums
   constexpr bool AHEAD = HELD + 16 * K <= ROOM, KEPT = AHEAD && HELD + 16 * K + 2 * VEC * K <= ROOM;
-  __shared__ float buf[2][16][8];
+  __shared__ float buf[2][128];
   __shared__ float fold[GROUPS > 1 ? GROUPS : 1][GROUPS > 1 ? LANES * VEC * K : 1];
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wave = w % W, grp = w / W;
@@ -241,10 +305,10 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
   // the gate row's rows
   const int gate_row = blockIdx.x / (uint32_t)a.slices, slice = blockIdx.x % (uint32_t)a.slices;
   const bool each = a.gate && a.span == 1;
-  const int64_t begin = each ? 0 : (int64_t)gate_row * a.span;
-  const int64_t end = each || a.rows - begin < a.span ? a.rows : begin + a.span;
-  const int64_t step = (int64_t)a.slices * GROUPS;
-  int64_t r = begin + (int64_t)slice * GROUPS + grp;
+  const int begin = each ? 0 : gate_row * a.span;
+  const int end = each || a.rows - begin < a.span ? a.rows : begin + a.span;
+  const int step = a.slices * GROUPS;
+  int r = begin + slice * GROUPS + grp;
   int turn = 0;
 
   auto col = [&](int k) { return VEC * (me + k * LANES); };
@@ -279,15 +343,26 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
     load_saved(y, a.y, row);
   };
 
-  float g1[KEPT ? K : 1][VEC], gp[KEPT ? K : 1][VEC];   // gamma; gate post_gamma
-  auto scales = [&](int k, float (&gm)[VEC], float (&pm)[VEC], int64_t row) {
-    load_values<DT>(a.gamma, a.wide_params, col(k), n, 1.f, gm);
-    load_values<DT>(a.post ? a.post_gamma : nullptr, a.wide_params, col(k), n, 1.f, pm);
+  // gamma and gate post_gamma, zero past the columns: what they multiply adds
+  // nothing to a sum there
+  float g1[KEPT ? K : 1][VEC], gp[KEPT ? K : 1][VEC];
+  auto cut = [&](int k, float (&v)[VEC]) {
+    if (col(k) + VEC > n)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) v[e] = col(k) + e < n ? v[e] : 0.f;
+  };
+  auto get_gamma = [&](int k, float (&v)[VEC]) {
+    load_values<DT>(a.gamma, a.wide_params, col(k), n, 1.f, v);
+    cut(k, v);
+  };
+  auto get_post = [&](int k, float (&v)[VEC]) {
+    load_values<DT>(a.post ? a.post_gamma : nullptr, a.wide_params, col(k), n, 1.f, v);
+    cut(k, v);
     if (!a.gate || each) return;
     float g[VEC];
     load_values<DT>(row_of(a.gate, a.wide_gate, gate_row, a.ldg, E), a.wide_gate, col(k), n, 1.f, g);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) pm[e] *= g[e];
+    for (int e = 0; e < VEC; ++e) v[e] *= g[e];
   };
   u32x4 nh[AHEAD ? K : 1], nd[AHEAD ? K : 1], nx[AHEAD ? K : 1], ny[AHEAD ? K : 1];
   if constexpr (AHEAD) {
@@ -297,7 +372,10 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
   }
   if constexpr (KEPT)
 #pragma unroll
-    for (int k = 0; k < K; ++k) scales(k, g1[k], gp[k], 0);
+    for (int k = 0; k < K; ++k) {
+      get_gamma(k, g1[k]);
+      get_post(k, gp[k]);
+    }
 
   float e0[K][VEC], e1[K][VEC], b0[K][VEC], b1[K][VEC];
 #pragma unroll
@@ -307,7 +385,7 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
 
   // every wave takes as many turns as the workgroup's first row needs; one past
   // the last row works on zeros and keeps nothing
-  for (int64_t first = begin + (int64_t)slice * GROUPS; first < end; first += step, r += step) {
+  for (int first = begin + slice * GROUPS; first < end; first += step, r += step) {
     const bool live = r < end;
     u32x4 dh[K], dr[K], x[K], y[K];
     if constexpr (AHEAD) {
@@ -323,9 +401,9 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
     open(y, a.y);
     // addresses and column tests made anew for each pass over a long row: kept
     // they would take a third of the registers
-    if constexpr (K * VEC > 16) asm volatile("" : "+v"(me));
+    if constexpr (K * VEC > 8) asm volatile("" : "+v"(me));
     float mx = 0.f, my = 0.f;
-    if (!a.rms) {
+    if constexpr (!RMS) {
       float s[2] = {0.f, 0.f};
 #pragma unroll
       for (int k = 0; k < K; ++k)
@@ -340,59 +418,90 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
     }
     keep_packed(x);
     keep_packed(y);
-    float q[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    // d = x - mx, f = y - my: d^2, t d, f^2; with the means d, t, f too
+    float q[RMS ? 3 : 6];
+#pragma unroll
+    for (float& v : q) v = 0.f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       float gm[VEC];
-      if constexpr (!KEPT) load_values<DT>(a.gamma, a.wide_params, col(k), n, 1.f, gm);
-      for_elems<VEC>(n - col(k), [&](int e) {
-        const float d = C::elem(x[k], e) - mx, f = C::elem(y[k], e) - my;
+      if constexpr (!KEPT) get_gamma(k, gm);
+      auto add = [&](int e) __attribute__((always_inline)) {
+        const float d = RMS ? C::elem(x[k], e) : C::elem(x[k], e) - mx;
+        const float f = RMS ? C::elem(y[k], e) : C::elem(y[k], e) - my;
         const float t = C::elem(dh[k], e) * (KEPT ? g1[KEPT ? k : 0][e] : gm[e]);
-        q[0] += d;
-        q[1] += d * d;
-        q[2] += t;
-        q[3] += t * d;
-        q[4] += f;
-        q[5] += f * f;
-      });
+        q[0] += d * d;
+        q[1] += t * d;
+        q[2] += f * f;
+        if constexpr (!RMS) {
+          q[3] += d;
+          q[4] += t;
+          q[5] += f;
+        }
+      };
+      if constexpr (RMS) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) add(e);
+      } else {
+        for_elems<VEC>(n - col(k), add);
+      }
     }
-    meet<W, 6>(q, buf, turn, wave, W * grp);
+    meet<W, RMS ? 3 : 6>(q, buf, turn, wave, W * grp);
     keep_packed(x);
     keep_packed(y);
     keep_packed(dh);
     keep_packed(dr);
     // (the mean's correction: see layernorm.hpp)
-    const float bx = a.rms ? 0.f : q[0] * inv, by = a.rms || !a.post ? 0.f : q[4] * inv;
-    const float rx = norm_rstd(q[1] * inv - bx * bx, a.eps);
-    const float ry = a.post ? norm_rstd(q[5] * inv - by * by, a.eps) : 1.f;
-    const float tbar = q[2] * inv, c1 = a.rms ? 0.f : tbar;
-    const float c2 = rx * (q[3] * inv - bx * tbar);   // mean(t rhat)
-    if constexpr (K * VEC > 16) asm volatile("" : "+v"(me));
+    float bx = 0.f, by = 0.f, tbar = 0.f;
+    if constexpr (!RMS) {
+      bx = q[3] * inv;
+      tbar = q[4] * inv;
+      by = a.post ? q[5] * inv : 0.f;
+    }
+    const float rx = norm_rstd(q[0] * inv - bx * bx, a.eps);
+    const float ry = a.post ? norm_rstd(q[2] * inv - by * by, a.eps) : 1.f;
+    // e = dr + rx t - rx mean(t) - rhat rx mean(t rhat)
+    const float c1 = rx * tbar, c2 = rx * (rx * (q[1] * inv - bx * tbar));
+    if constexpr (K * VEC > 8) asm volatile("" : "+v"(me));
     float ev[K][VEC];
-    float s[2] = {0.f, 0.f};
+    float s[RMS ? 1 : 2];
+#pragma unroll
+    for (float& v : s) v = 0.f;
     char* p = static_cast<char*>(a.out_r) + r * a.ld_r * (int64_t)E;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       float gm[VEC], pm[VEC];
-      if constexpr (!KEPT) scales(k, gm, pm, 0);
-      float out[VEC], gate[VEC];
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float h = C::elem(dh[k], e), xh = ((C::elem(x[k], e) - mx) - bx) * rx;
-        float v = C::elem(dr[k], e);
-        if (a.dh) v += rx * ((h * (KEPT ? g1[KEPT ? k : 0][e] : gm[e]) - c1) - xh * c2);
-        ev[k][e] = v;
-        out[e] = a.alpha * v;
-        if (live) {
-          b0[k][e] += h;
-          b1[k][e] += h * xh;
-        }
+      if constexpr (!KEPT) {
+        get_gamma(k, gm);
+        get_post(k, pm);
       }
-      if (live && col(k) < n) C::store(p, col(k), n, out);
+      float out[VEC];
+      if (a.dh) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float h = C::elem(dh[k], e), t = h * (KEPT ? g1[KEPT ? k : 0][e] : gm[e]);
+          const float xh = (RMS ? C::elem(x[k], e) : (C::elem(x[k], e) - mx) - bx) * rx;
+          float v = C::elem(dr[k], e) + rx * t;
+          if constexpr (!RMS) v -= c1;
+          ev[k][e] = v - xh * c2;
+          if (live) {
+            b0[k][e] += h;
+            b1[k][e] += h * xh;
+          }
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) ev[k][e] = C::elem(dr[k], e);
+      }
+      if (live && col(k) < n) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) out[e] = a.alpha * ev[k][e];
+        C::store(p, col(k), n, out);
+      }
       if (each) {
         // the gate's own gradient, and the gate into e
-        const int64_t at = live ? r : 0;
-        load_values<DT>(row_of(a.gate, a.wide_gate, at, a.ldg, E), a.wide_gate, col(k), n, 1.f, gate);
+        float gate[VEC];
+        load_values<DT>(row_of(a.gate, a.wide_gate, live ? r : 0, a.ldg, E), a.wide_gate, col(k), n, 1.f, gate);
         if (a.dgate && live && col(k) < n) {
           float pg[VEC], pb[VEC];
           load_values<DT>(a.post ? a.post_gamma : nullptr, a.wide_params, col(k), n, 1.f, pg);
@@ -416,26 +525,35 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
 #pragma unroll
         for (int e = 0; e < VEC; ++e) ev[k][e] *= gate[e];
       }
-      for_elems<VEC>(n - col(k), [&](int e) {
-        const float f = C::elem(y[k], e) - my, sv = ev[k][e] * (KEPT ? gp[KEPT ? k : 0][e] : pm[e]);
-        s[0] += sv;
-        s[1] += sv * f;
-      });
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float f = RMS ? C::elem(y[k], e) : C::elem(y[k], e) - my;
+        const float sv = ev[k][e] * (KEPT ? gp[KEPT ? k : 0][e] : pm[e]);
+        s[0] += sv * f;
+        if constexpr (!RMS) s[1] += sv;
+      }
     }
-    if (a.post) meet<W, 2>(s, buf, turn, wave, W * grp);
+    if (a.post) meet<W, RMS ? 1 : 2>(s, buf, turn, wave, W * grp);
     keep_packed(y);
     if (!live) continue;
-    const float sbar = s[0] * inv, s1 = a.rms || !a.post ? 0.f : sbar;
-    const float s2 = a.post ? ry * (s[1] * inv - by * sbar) : 0.f;   // mean(s yhat)
+    // dy = ry s - ry mean(s) - yhat ry mean(s yhat)
+    float s1 = 0.f, s2 = 0.f;
+    if (a.post) {
+      const float sbar = RMS ? 0.f : s[RMS ? 0 : 1] * inv;
+      s1 = ry * sbar;
+      s2 = ry * (ry * (s[0] * inv - by * sbar));
+    }
     p = static_cast<char*>(a.out_y) + r * a.ld_y * (int64_t)E;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      float gm[VEC], pm[VEC], out[VEC];
-      if constexpr (!KEPT) scales(k, gm, pm, 0);
+      float pm[VEC], out[VEC];
+      if constexpr (!KEPT) get_post(k, pm);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        const float yh = ((C::elem(y[k], e) - my) - by) * ry, v = ev[k][e];
-        out[e] = ry * ((v * (KEPT ? gp[KEPT ? k : 0][e] : pm[e]) - s1) - yh * s2);
+        const float yh = (RMS ? C::elem(y[k], e) : (C::elem(y[k], e) - my) - by) * ry, v = ev[k][e];
+        float o = ry * (v * (KEPT ? gp[KEPT ? k : 0][e] : pm[e]));
+        if constexpr (!RMS) o -= s1;
+        out[e] = o - yh * s2;
         e0[k][e] += v;
         e1[k][e] += v * yh;
       }
