@@ -711,8 +711,8 @@ trt_status trt_act8_weight_grad(int64_t tokens, int64_t outputs, int64_t inputs,
  * TRT_F32), leading dimensions in elements: inputs >= 1, outputs >= cols.  h may be
  * NULL (no norm follows); dh or dr_out may be NULL (zero), not both; without dh
  * r_out is not read and may be NULL, and dgamma and dbeta are refused.  In the
- * backward pass r_out and y may each be 8-bit rows of trt_act8_pack (scale not
- * NULL), read as trt_act8_unpack gives them in dtype.
+ * backward pass r_out and y may both be 8-bit rows of trt_act8_pack (scale not
+ * NULL; TRT_ERR_ARG for one of them), read as trt_act8_unpack gives them in dtype.
  *
  * gate: [ceil(rows / rows_per_gate), cols] of gate_dtype, row i of the block under
  * gate row i / rows_per_gate: one gate for all rows, one for each sequence, one

@@ -75,12 +75,13 @@ def test_forward_refusals(kw, code):
     (dict(wsb=3 * 4 * 64 * 4 - 1), trt.ERR_SIZE), (dict(wsb=-1), trt.ERR_SIZE), (dict(ws=BASE * 30 + 8), trt.ERR_ALIGN),
     (dict(post=0, post_gamma=0, post_beta=0), trt.ERR_ARG), (dict(post=0, post_gamma=0, post_beta=0, dpg=0), trt.ERR_ARG),
     (dict(lddh=0), trt.ERR_STRIDE), (dict(lddr=63), trt.ERR_STRIDE), (dict(lddy=63), trt.ERR_STRIDE), (dict(lddg=63), trt.ERR_STRIDE),
-    (dict(ldr=0), trt.ERR_STRIDE), (dict(ys=BASE * 7, yls=0), trt.ERR_STRIDE),
+    (dict(ldr=0), trt.ERR_STRIDE), (dict(rs=BASE * 8, ys=BASE * 7, yls=0), trt.ERR_STRIDE),
+    (dict(rs=BASE * 8), trt.ERR_ARG), (dict(ys=BASE * 8), trt.ERR_ARG),          # one of them in 8 bits
     (dict(dh=BASE + 1), trt.ERR_ALIGN), (dict(r=BASE * 3 + 1), trt.ERR_ALIGN), (dict(dgate=BASE * 20 + 1), trt.ERR_ALIGN),
     (dict(dr=BASE), trt.ERR_OVERLAP), (dict(dy=BASE * 2), trt.ERR_OVERLAP), (dict(dr=BASE * 3), trt.ERR_OVERLAP),
     (dict(dy=BASE * 4), trt.ERR_OVERLAP), (dict(dy=BASE * 5), trt.ERR_OVERLAP), (dict(dgate=BASE * 10), trt.ERR_OVERLAP),
     (dict(dpg=BASE * 11), trt.ERR_OVERLAP), (dict(db=BASE * 23), trt.ERR_OVERLAP), (dict(ws=BASE * 2), trt.ERR_OVERLAP),
-    (dict(rs=BASE * 7, dy=BASE * 7), trt.ERR_OVERLAP), (dict(ys=BASE * 7, dr=BASE * 7 - 2), trt.ERR_OVERLAP),
+    (dict(rs=BASE * 7, ys=BASE * 8, dy=BASE * 7), trt.ERR_OVERLAP), (dict(rs=BASE * 8, ys=BASE * 7, dr=BASE * 7 - 2), trt.ERR_OVERLAP),
     (dict(cols=16385, lddh=20000, lddro=20000, ldr=20000, ldy=20000, lddr=20000, lddy=20000, lddg=20000), trt.ERR_UNSUPPORTED),
     (dict(rows=1 << 24, rows_per_gate=2), trt.ERR_SIZE),
 ])
@@ -91,7 +92,7 @@ def test_backward_refusals(kw, code):
 
 def test_an_8_bit_row_needs_no_alignment():
     # (refused later, for the overlap, so that nothing is launched)
-    assert backward(rs=BASE * 7 + 1, r=BASE * 3 + 1, dr=BASE) == trt.ERR_OVERLAP
+    assert backward(rs=BASE * 7 + 1, ys=BASE * 8 + 1, r=BASE * 3 + 1, dr=BASE) == trt.ERR_OVERLAP
 
 
 def test_workspace_size():

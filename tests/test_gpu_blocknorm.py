@@ -284,8 +284,8 @@ def test_leading_dimensions_and_broadcast_gates():
         a = trt.block_norm(x, y, gate)
         b = trt.block_norm(x.view(15, 40), y.view(15, 40), gate.reshape(-1, 40), rows_per_gate=rows)
         assert all(torch.equal(p.view(15, 40), q) for p, q in zip(a, b))
-        a = trt.block_norm_bwd(x, y, x, (trt.act8_pack(y)), gate)
-        b = trt.block_norm_bwd(x.view(15, 40), y.view(15, 40), x.view(15, 40), trt.act8_pack(y.view(15, 40)), gate.reshape(-1, 40),
+        a = trt.block_norm_bwd(x, y, trt.act8_pack(x), trt.act8_pack(y), gate)
+        b = trt.block_norm_bwd(x.view(15, 40), y.view(15, 40), trt.act8_pack(x.view(15, 40)), trt.act8_pack(y.view(15, 40)), gate.reshape(-1, 40),
                                rows_per_gate=rows)
         assert a[2].shape == gate.shape
         assert all(torch.equal(p.reshape(q.shape), q) for p, q in zip(a, b))
@@ -349,7 +349,7 @@ def test_graph_on_a_stream_of_its_own():
 
     def work():
         out, h = trt.block_norm(x, y, gate, **kw)
-        return out, h, *trt.block_norm_bwd(dh, dr, out, trt.act8_pack(y), gate, workspace=ws, **kw)
+        return out, h, *trt.block_norm_bwd(dh, dr, trt.act8_pack(out), trt.act8_pack(y), gate, workspace=ws, **kw)
 
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):
@@ -364,6 +364,6 @@ def test_graph_on_a_stream_of_its_own():
         torch.cuda.synchronize()
         graph.replay()
         out, h = trt.block_norm(x, y, gate, **kw)
-        eager = (out, h, *trt.block_norm_bwd(dh, dr, out, trt.act8_pack(y), gate, **kw))
+        eager = (out, h, *trt.block_norm_bwd(dh, dr, trt.act8_pack(out), trt.act8_pack(y), gate, **kw))
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(captured, eager)), turn

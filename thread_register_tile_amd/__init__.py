@@ -1087,7 +1087,7 @@ def block_norm_bwd(dh, dr_out, r_out, y, gate=None, *, post=True, post_gamma=Non
     """The gradients of block_norm for dh and dr_out, those of its results:
     (dr, dy, dgate, dpost_gamma, dpost_beta, dgamma, dbeta), by
     trt_block_norm_bwd.  Either of dh and dr_out may be None (zero); r_out is
-    the forward pass's result, y its input, each a tensor or the (q, scale) of
+    the forward pass's result, y its input, both tensors or both the (q, scale) of
     act8_pack, read as act8_unpack gives them in dh's dtype; r_out may be None
     without dh.  The other arguments are the forward pass's (the gradients do not
     depend on beta).  dgate is None without a gate, dpost_gamma and dpost_beta

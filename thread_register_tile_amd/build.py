@@ -19,7 +19,8 @@ SOURCES = ["trt.hip", "kern_tiny.hip", "kern_64.hip", "kern_128.hip", "kern_256.
            "kern_xent.hip", "kern_xent_stats.hip", "kern_xent_grad.hip", "kern_xent_input.hip",
            "kern_xent_weight.hip", "trt_act8.hip", "kern_act8.hip", "kern_act8_weight.hip",
            "trt_blocknorm.hip", "kern_blocknorm.hip", "kern_blocknorm_bwd_f16.hip",
-           "kern_blocknorm_bwd_bf16.hip", "kern_blocknorm_bwd_f32.hip"]
+           "kern_blocknorm_bwd_bf16.hip", "kern_blocknorm_bwd_f32.hip", "kern_blocknorm_bwd_f16_8bit.hip",
+           "kern_blocknorm_bwd_bf16_8bit.hip", "kern_blocknorm_bwd_f32_8bit.hip"]
 # Per-file flags.  The binary32 kernels keep their accumulators in ordinary
 # VGPRs: left to itself the compiler puts them in AGPRs and moves half of
 # them through VGPRs every K step.

@@ -38,15 +38,123 @@
 
 namespace trt {
 
-// VEC values from element i of p, binary32 or of the rows' type.
-template <int DT, int VEC>
-__device__ __forceinline__ void load_values(const void* p, bool wide, int i, int n, float absent, float (&v)[VEC]) {
-  if (DT == DT_F32 || wide) load_params<DT_F32>(p, i, n, absent, v);
-  else load_params<DT>(p, i, n, absent, v);
+__device__ __forceinline__ const char* row_of(const void* p, bool wide, int64_t row, int64_t ld, int narrow) {
+  return static_cast<const char*>(p) + row * ld * (wide ? 4 : narrow);
 }
 
-__device__ __forceinline__ const void* row_of(const void* p, bool wide, int64_t row, int64_t ld, int narrow) {
-  return static_cast<const char*>(p) + row * ld * (wide ? 4 : narrow);
+// A row's chunks without a branch: with memory operations under a condition the
+// compiler counts the fewest that may be in flight, and a wait for the row at
+// work then waits for the next one's loads or the last one's stores too (16384 x
+// 8192 bf16 backward from 8-bit rows 400 us, 280 without).  A row of n >= VEC
+// elements is read VEC at a time from no further than its last VEC, and `fix`
+// shifts out what lies before the chunk (all of it, where the chunk lies past the
+// row): zeros take its place.  Stores go through a descriptor of the row, at an
+// offset beyond it where the chunk is not whole; the cut chunk of a row whose
+// length VEC does not divide follows element by element.
+// TINY: rows of fewer than VEC elements, read one by one.
+template <int DT, bool TINY>
+struct RowIO {
+  using C = RowChunk<DT>;
+  using Q = Act8Chunk<DT>;
+  static constexpr int VEC = C::VEC, E = sizeof(typename C::Elem), BITS = 8 * E;
+
+  __device__ static u32x4 load(const char* row, int i, int n) {
+    if constexpr (TINY) return i < n ? C::load(row, i, n) : u32x4{0u, 0u, 0u, 0u};
+    const int at = i < n - VEC ? i : n - VEC;
+    return __builtin_nontemporal_load(reinterpret_cast<const typename C::Word4*>(row + at * E));
+  }
+  __device__ static u32x4 load_shared(const char* row, int i, int n) {
+    if constexpr (TINY) return i < n ? C::load_shared(row, i, n) : u32x4{0u, 0u, 0u, 0u};
+    const int at = i < n - VEC ? i : n - VEC;
+    return *reinterpret_cast<const typename C::Word4*>(row + at * E);
+  }
+  __device__ static u32x2 load8(const int8_t* row, int i, int n) {
+    if constexpr (TINY) return i < n ? Q::load(row, i, n) : u32x2{0u, 0u};
+    const int8_t* p = row + (i < n - VEC ? i : n - VEC);
+    if constexpr (VEC == 8) return __builtin_nontemporal_load(reinterpret_cast<const u32x2_at1*>(p));
+    else return u32x2{__builtin_nontemporal_load(reinterpret_cast<const u32_at1*>(p)), 0u};
+  }
+
+  // The chunk's own elements, of `over` (0 to VEC) that came before it.
+  __device__ static int over(int i, int n) {
+    const int o = i + VEC - n;
+    return o < 0 ? 0 : o < VEC ? o : VEC;
+  }
+  __device__ static u32x4 fix(u32x4 v, int i, int n) {
+    if constexpr (TINY) return v;
+    const int bits = over(i, n) * BITS, b = bits & 63;
+    const uint64_t lo = v[0] | (uint64_t)v[1] << 32, hi = v[2] | (uint64_t)v[3] << 32;
+    const uint64_t l = bits & 64 ? hi : lo, h = bits & 64 ? 0 : hi;
+    uint64_t a = l >> b | h << 1 << (63 - b), c = h >> b;
+    if (bits == 128) a = c = 0;
+    return u32x4{(uint32_t)a, (uint32_t)(a >> 32), (uint32_t)c, (uint32_t)(c >> 32)};
+  }
+  __device__ static u32x2 fix8(u32x2 v, int i, int n) {
+    if constexpr (TINY) return v;
+    const int bits = over(i, n) * 8;   // of VEC bytes: 64, or 32 with nothing above them
+    const uint64_t q = v[0] | (uint64_t)v[1] << 32, a = bits == 64 ? 0 : q >> bits;
+    return u32x2{(uint32_t)a, (uint32_t)(a >> 32)};
+  }
+
+  // whole: no chunk of the wave is cut.  live: store at all.
+  __device__ static void store(char* row, int i, int n, bool whole, bool live, const float (&y)[VEC]) {
+    const auto rs = __builtin_amdgcn_make_buffer_rsrc((void*)row, (short)0, live ? n * E : 0, kBufferFormat);
+    u32x4 v;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      if constexpr (DT == DT_F32) v[w] = __float_as_uint(y[w]);
+      else v[w] = pack2_f32<DT>(y[2 * w], y[2 * w + 1]);
+    }
+    const uint32_t off = (uint32_t)i * E;
+    __builtin_amdgcn_raw_buffer_store_b128(v, rs, (int)(off | (i + VEC <= n ? 0u : 0x80000000u)), 0, kNonTemporal);
+    if (whole || n % VEC == 0) return;
+    const bool cut = i < n && i + VEC > n;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      const int at = (int)((off + e * E) | (cut && i + e < n ? 0u : 0x80000000u));
+      if constexpr (DT == DT_F32) __builtin_amdgcn_raw_buffer_store_b32(v[e], rs, at, 0, 0);
+      else __builtin_amdgcn_raw_buffer_store_b16((short)(v[e / 2] >> (16 * (e & 1))), rs, at, 0, 0);
+    }
+  }
+};
+
+// VEC values of a vector or of a gate's row, of the rows' type or binary32;
+// `absent` where there is none, else zero past n.  (Read by many workgroups.)
+template <int DT, bool TINY>
+__device__ __forceinline__ void load_values(const void* p, bool wide, int i, int n, bool whole, float absent,
+                                            float (&v)[RowChunk<DT>::VEC]) {
+  using F = RowIO<DT_F32, TINY>;
+  using IO = RowIO<DT, TINY>;
+  constexpr int VEC = RowChunk<DT>::VEC;
+  if (!p) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) v[e] = absent;
+  } else if (DT == DT_F32 || wide) {
+#pragma unroll
+    for (int c = 0; c < VEC; c += 4) {
+      u32x4 x = F::load_shared(static_cast<const char*>(p), i + c, n);
+      if (!whole) x = F::fix(x, i + c, n);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[c + e] = __uint_as_float(x[e]);
+    }
+  } else {
+    u32x4 x = IO::load_shared(static_cast<const char*>(p), i, n);
+    if (!whole) x = IO::fix(x, i, n);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) v[e] = RowChunk<DT>::elem(x, e);
+  }
+}
+
+// 1 / sqrt(v + eps) as norm_rstd gives it (NaN stays NaN, a v that rounding left
+// below zero counts as zero) but by the reciprocal square root instruction, which
+// is off by at most one unit in the last place where its argument is not below
+// the normal numbers: those are scaled by 2^100.  (The two square roots and
+// divisions of a row took a twentieth of the backward pass's instructions.)
+__device__ __forceinline__ float block_rstd(float v, float eps) {
+  const float x = (v < 0.f ? 0.f : v) + eps;
+  const bool small = x < 0x1p-100f;
+  const float y = __builtin_amdgcn_rsqf(small ? x * 0x1p100f : x);
+  return small ? y * 0x1p50f : y;
 }
 
 // Sums of several values at once.  Each step that halves the lanes of one value's
@@ -136,9 +244,10 @@ __device__ __forceinline__ void meet(float (&v)[N], float (*buf)[128], int& turn
 // EACH: a gate of its own for every row, loaded with it; otherwise gate and
 // post norm's parameters are one product, made again when the gate row changes.
 // KEEP: the vectors stay in registers (of 16 waves to a row none are left).
-template <int DT, int W, int K, bool EACH>
+template <int DT, int W, int K, bool EACH, bool TINY>
 __global__ __launch_bounds__(NormShape<W>::THREADS) void block_norm_kernel(BlockNormArgs a) {
   using C = RowChunk<DT>;
+  using IO = RowIO<DT, TINY>;
   constexpr int VEC = C::VEC, LANES = 64 * W, GROUPS = NormShape<W>::GROUPS, E = sizeof(typename C::Elem);
   constexpr bool KEEP = W < 16;
   __shared__ float buf[2][128];
@@ -148,56 +257,61 @@ __global__ __launch_bounds__(NormShape<W>::THREADS) void block_norm_kernel(Block
   const int me = 64 * wave + (threadIdx.x & 63);
   const int n = a.cols;
   const float inv = 1.f / (float)a.cols;
-  const int64_t step = (int64_t)gridDim.x * GROUPS;
-  int64_t r = (int64_t)blockIdx.x * GROUPS + grp;
+  // a row of workgroups at a time, each of which has a row in every turn
+  const int step = gridDim.x * GROUPS;
+  int r = blockIdx.x * GROUPS + grp;
   int turn = 0;
 
   auto col = [&](int k) { return VEC * (me + k * LANES); };
-  auto load = [&](u32x4 (&v)[K], const SavedRows& x, int64_t row) {
-    const char* p = static_cast<const char*>(x.x) + row * x.ld * (int64_t)E;
-#pragma unroll
-    for (int k = 0; k < K; ++k) v[k] = col(k) < n ? C::load(p, col(k), n) : u32x4{0u, 0u, 0u, 0u};
-  };
+  auto whole = [&](int k) { return VEC * (64 * (wave + 1) + k * LANES) <= n; };   // a scalar
 
   // u1 yhat + u0 is what the gate multiplies (EACH) or what joins the stream
   float u1[KEEP ? K : 1][VEC], u0[KEEP ? K : 1][VEC], gamma[KEEP ? K : 1][VEC], beta[KEEP ? K : 1][VEC];
   auto post = [&](int k, int to, int64_t gate_row) {
-    load_values<DT>(a.post ? a.post_gamma : nullptr, a.wide_params, col(k), n, 1.f, u1[to]);
-    load_values<DT>(a.post ? a.post_beta : nullptr, a.wide_params, col(k), n, 0.f, u0[to]);
+    load_values<DT, TINY>(a.post ? a.post_gamma : nullptr, a.wide_params, col(k), n, whole(k), 1.f, u1[to]);
+    load_values<DT, TINY>(a.post ? a.post_beta : nullptr, a.wide_params, col(k), n, whole(k), 0.f, u0[to]);
     if (!EACH && a.gate) {
       float g[VEC];
-      load_values<DT>(row_of(a.gate, a.wide_gate, gate_row, a.ldg, E), a.wide_gate, col(k), n, 1.f, g);
+      load_values<DT, TINY>(row_of(a.gate, a.wide_gate, gate_row, a.ldg, E), a.wide_gate, col(k), n, whole(k), 1.f, g);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) u1[to][e] *= g[e], u0[to][e] *= g[e];
     }
   };
   auto pre = [&](int k, int to) {
-    load_values<DT>(a.gamma, a.wide_params, col(k), n, 1.f, gamma[to]);
-    load_values<DT>(a.beta, a.wide_params, col(k), n, 0.f, beta[to]);
+    load_values<DT, TINY>(a.gamma, a.wide_params, col(k), n, whole(k), 1.f, gamma[to]);
+    load_values<DT, TINY>(a.beta, a.wide_params, col(k), n, whole(k), 0.f, beta[to]);
   };
 
-  u32x4 nr[K], ny[K];
-  if (r < a.rows) {
-    load(nr, a.r, r);
-    load(ny, a.y, r);
-  }
+  // two rows' registers, used in turn: the one at work and the one on its way
+  struct Row {
+    u32x4 x[K], y[K];
+  };
+  Row rows[2];
+  auto load_row = [&](Row& q, int row) __attribute__((always_inline)) {
+    row = row < a.rows ? row : a.rows - 1;
+    const char *x = row_of(a.r.x, false, row, a.r.ld, E), *y = row_of(a.y.x, false, row, a.y.ld, E);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      q.x[k] = IO::load(x, col(k), n);
+      q.y[k] = IO::load(y, col(k), n);
+    }
+  };
+  load_row(rows[0], r);
   if constexpr (KEEP)
 #pragma unroll
     for (int k = 0; k < K; ++k) pre(k, k);
   int64_t gate_row = -1;
-  for (; r < a.rows; r += step) {
-    u32x4 x[K], y[K];
-#pragma unroll
-    for (int k = 0; k < K; ++k) x[k] = nr[k], y[k] = ny[k];
+  auto body = [&](Row& row, Row& next) __attribute__((always_inline)) {
+    auto &x = row.x, &y = row.y;
     float g[EACH ? K : 1][VEC];
     if constexpr (EACH)
 #pragma unroll
       for (int k = 0; k < K; ++k)
-        load_values<DT>(row_of(a.gate, a.wide_gate, r, a.ldg, E), a.wide_gate, col(k), n, 1.f, g[k]);
-    if (r + step < a.rows) {
-      load(nr, a.r, r + step);
-      load(ny, a.y, r + step);
-    }
+        load_values<DT, TINY>(row_of(a.gate, a.wide_gate, r, a.ldg, E), a.wide_gate, col(k), n, whole(k), 1.f, g[k]);
+    load_row(next, r + step);
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (!whole(k)) x[k] = IO::fix(x[k], col(k), n), y[k] = IO::fix(y[k], col(k), n);
     const int64_t at = EACH ? 0 : (int64_t)((uint32_t)r / (uint32_t)a.span);
     if constexpr (KEEP)
       if (at != gate_row) {
@@ -229,7 +343,7 @@ __global__ __launch_bounds__(NormShape<W>::THREADS) void block_norm_kernel(Block
       meet<W, 2>(q, buf, turn, wave, W * grp);
       keep_packed(y);
       dbar = a.rms ? 0.f : q[0] * inv;
-      rstd = norm_rstd(q[1] * inv - dbar * dbar, a.eps);
+      rstd = block_rstd(q[1] * inv - dbar * dbar, a.eps);
     }
     // the stream, zero past the columns
     float z[K][VEC];
@@ -247,9 +361,8 @@ __global__ __launch_bounds__(NormShape<W>::THREADS) void block_norm_kernel(Block
         z[k][e] = rounded(a.alpha * C::elem(x[k], e) + u);
         s[0] += z[k][e];
       });
-      if (col(k) < n) C::store(p, col(k), n, z[k]);
+      IO::store(p, col(k), n, whole(k), true, z[k]);
     }
-    if (!a.out_y) continue;
     m = dbar = 0.f;
     if (!a.rms) {
       meet<W, 1>(s, buf, turn, wave, W * grp);
@@ -265,18 +378,24 @@ __global__ __launch_bounds__(NormShape<W>::THREADS) void block_norm_kernel(Block
       });
     meet<W, 2>(q, buf, turn, wave, W * grp);
     dbar = a.rms ? 0.f : q[0] * inv;
-    rstd = norm_rstd(q[1] * inv - dbar * dbar, a.eps);
+    rstd = block_rstd(q[1] * inv - dbar * dbar, a.eps);
+    // (no h asked for: a descriptor of no bytes)
     p = static_cast<char*>(a.out_y) + r * a.ld_y * (int64_t)E;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      if (col(k) >= n) continue;
       const int to = KEEP ? k : 0;
       if constexpr (!KEEP) pre(k, 0);
       float h[VEC];
 #pragma unroll
       for (int e = 0; e < VEC; ++e) h[e] = ((z[k][e] - m) - dbar) * rstd * gamma[to][e] + beta[to][e];
-      C::store(p, col(k), n, h);
+      IO::store(p, col(k), n, whole(k), a.out_y, h);
     }
+  };
+  for (; r < a.rows; r += step) {
+    body(rows[0], rows[1]);
+    r += step;
+    if (r >= a.rows) break;
+    body(rows[1], rows[0]);
   }
 }
 
@@ -287,10 +406,11 @@ __global__ __launch_bounds__(NormShape<W>::THREADS) void block_norm_kernel(Block
 // which with 8-bit rows takes as long as the memory).
 // AHEAD: the next row is loaded ahead, KEPT: gamma and post_gamma stay in
 // registers, where the sums leave room for them.
-template <int DT, int W, int K, int WAVES, bool RMS>
+template <int DT, bool BYTES, int W, int K, int WAVES, bool RMS, bool TINY>
 __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArgs a) {
   using C = RowChunk<DT>;
   using Q = Act8Chunk<DT>;
+  using IO = RowIO<DT, TINY>;
   constexpr int VEC = C::VEC, LANES = 64 * W, GROUPS = WAVES / W, E = sizeof(typename C::Elem);
   constexpr int ROOM = WAVES <= 8 ? 216 : 0;         // of 256 registers (168 and 128 of 12 and 16 waves)
   constexpr int HELD = K * (16 + 5 * VEC);           // the rows, e and the sums
@@ -312,35 +432,54 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
   int turn = 0;
 
   auto col = [&](int k) { return VEC * (me + k * LANES); };
-  const u32x4 none = {0u, 0u, 0u, 0u};
-  auto load = [&](u32x4 (&v)[K], const void* base, int64_t ld, int64_t row) {
-    const char* p = static_cast<const char*>(base) + row * ld * (int64_t)E;
-#pragma unroll
-    for (int k = 0; k < K; ++k) v[k] = base && col(k) < n ? C::load(p, col(k), n) : none;
+  auto whole = [&](int k) { return VEC * (64 * (wave + 1) + k * LANES) <= n; };   // a scalar
+  using Saved = std::conditional_t<BYTES, u32x2, u32x4>;
+  struct Row {
+    u32x4 dh[K], dr[K];
+    Saved x[K], y[K];
+    uint32_t xb[K], yb[K];   // BYTES: the scales' bytes
   };
-  // 8-bit rows wait as their bytes and the scale's
-  auto load_saved = [&](u32x4 (&v)[K], const SavedRows& x, int64_t row) {
-    if (!x.scale) return load(v, x.x, x.ld, row);
-    const int8_t* p = static_cast<const int8_t*>(x.x) + row * x.ld;
-    const uint8_t* s = x.scale + row * x.lds;
+  // The operations are as many whatever there is to load: without dh or dr the
+  // other stands for it, and for r'.
+  const u32x4 none = {0u, 0u, 0u, 0u};
+  const char *dhp = static_cast<const char*>(a.dh ? a.dh : a.dr), *drp = static_cast<const char*>(a.dr ? a.dr : a.dh);
+  const int64_t lddh = a.dh ? a.lddh : a.lddr, lddr = a.dr ? a.lddr : a.lddh;
+  const SavedRows xs = a.dh ? a.r : a.y, ys = a.y;
+  auto load_saved = [&](Saved (&v)[K], uint32_t (&b)[K], const SavedRows& x, int row) __attribute__((always_inline)) {
+    const char* p = static_cast<const char*>(x.x) + row * x.ld * (int64_t)(BYTES ? 1 : E);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      v[k] = none;
-      if (col(k) >= n) continue;
-      const u32x2 q = Q::load(p, col(k), n);
-      v[k] = u32x4{q[0], q[1], s[col(k) / kAct8Block], 0u};
+      if constexpr (BYTES) {
+        const int at = col(k) < n ? col(k) : n - 1;
+        v[k] = IO::load8(reinterpret_cast<const int8_t*>(p), col(k), n);
+        b[k] = (x.scale + row * x.lds)[at / kAct8Block];
+      } else {
+        v[k] = IO::load(p, col(k), n);
+      }
     }
   };
-  auto open = [&](u32x4 (&v)[K], const SavedRows& x) {
-    if (!x.scale) return;
+  auto load_row = [&](Row& q, int row) __attribute__((always_inline)) {
+    row = row < end ? row : end - 1;
 #pragma unroll
-    for (int k = 0; k < K; ++k) v[k] = Q::restore(u32x2{v[k][0], v[k][1]}, Q::step(v[k][2]));
+    for (int k = 0; k < K; ++k) {
+      q.dh[k] = IO::load(dhp + row * lddh * (int64_t)E, col(k), n);
+      q.dr[k] = IO::load(drp + row * lddr * (int64_t)E, col(k), n);
+    }
+    load_saved(q.x, q.xb, xs, row);
+    load_saved(q.y, q.yb, ys, row);
   };
-  auto load_row = [&](u32x4 (&dh)[K], u32x4 (&dr)[K], u32x4 (&x)[K], u32x4 (&y)[K], int64_t row) {
-    load(dh, a.dh, a.lddh, row);
-    load(dr, a.dr, a.lddr, row);
-    load_saved(x, a.r, row);
-    load_saved(y, a.y, row);
+  auto open_saved = [&](u32x4 (&to)[K], const Saved (&v)[K], const uint32_t (&b)[K]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if constexpr (BYTES) {
+        u32x2 q = v[k];
+        if (!whole(k)) q = IO::fix8(q, col(k), n);
+        to[k] = Q::restore(q, Q::step(b[k]));
+      } else {
+        to[k] = v[k];
+        if (!whole(k)) to[k] = IO::fix(to[k], col(k), n);
+      }
+    }
   };
 
   // gamma and gate post_gamma, zero past the columns: what they multiply adds
@@ -352,24 +491,21 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
       for (int e = 0; e < VEC; ++e) v[e] = col(k) + e < n ? v[e] : 0.f;
   };
   auto get_gamma = [&](int k, float (&v)[VEC]) {
-    load_values<DT>(a.gamma, a.wide_params, col(k), n, 1.f, v);
+    load_values<DT, TINY>(a.gamma, a.wide_params, col(k), n, whole(k), 1.f, v);
     cut(k, v);
   };
   auto get_post = [&](int k, float (&v)[VEC]) {
-    load_values<DT>(a.post ? a.post_gamma : nullptr, a.wide_params, col(k), n, 1.f, v);
+    load_values<DT, TINY>(a.post ? a.post_gamma : nullptr, a.wide_params, col(k), n, whole(k), 1.f, v);
     cut(k, v);
     if (!a.gate || each) return;
     float g[VEC];
-    load_values<DT>(row_of(a.gate, a.wide_gate, gate_row, a.ldg, E), a.wide_gate, col(k), n, 1.f, g);
+    load_values<DT, TINY>(row_of(a.gate, a.wide_gate, gate_row, a.ldg, E), a.wide_gate, col(k), n, whole(k), 1.f, g);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) v[e] *= g[e];
   };
-  u32x4 nh[AHEAD ? K : 1], nd[AHEAD ? K : 1], nx[AHEAD ? K : 1], ny[AHEAD ? K : 1];
-  if constexpr (AHEAD) {
-#pragma unroll
-    for (int k = 0; k < K; ++k) nh[k] = nd[k] = nx[k] = ny[k] = none;
-    if (r < end) load_row(nh, nd, nx, ny, r);
-  }
+  // two rows' registers, used in turn: the one at work and the one on its way
+  Row rows[AHEAD ? 2 : 1];
+  if constexpr (AHEAD) load_row(rows[0], r);
   if constexpr (KEPT)
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -383,22 +519,23 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
 #pragma unroll
     for (int e = 0; e < VEC; ++e) e0[k][e] = e1[k][e] = b0[k][e] = b1[k][e] = 0.f;
 
-  // every wave takes as many turns as the workgroup's first row needs; one past
-  // the last row works on zeros and keeps nothing
-  for (int first = begin + slice * GROUPS; first < end; first += step, r += step) {
-    const bool live = r < end;
-    u32x4 dh[K], dr[K], x[K], y[K];
-    if constexpr (AHEAD) {
+  // One row; a wave whose row lies past the end works on zeros, with rstd = 0, and
+  // stores nothing.
+  auto body = [&](Row& row, Row& next) __attribute__((always_inline)) {
+    const bool live = GROUPS == 1 || r < end;
+    load_row(AHEAD ? next : row, AHEAD ? r + step : r);
+    u32x4 (&dh)[K] = row.dh, (&dr)[K] = row.dr, x[K], y[K];
 #pragma unroll
-      for (int k = 0; k < K; ++k) dh[k] = nh[k], dr[k] = nd[k], x[k] = nx[k], y[k] = ny[k];
-      if (r + step < end) load_row(nh, nd, nx, ny, r + step);
-    } else {
+    for (int k = 0; k < K; ++k)
+      if (!whole(k)) dh[k] = IO::fix(dh[k], col(k), n), dr[k] = IO::fix(dr[k], col(k), n);
+    open_saved(x, row.x, row.xb);
+    open_saved(y, row.y, row.yb);
+    if (!a.dr)
+#pragma unroll
+      for (int k = 0; k < K; ++k) dr[k] = none;
+    if (!live)
 #pragma unroll
       for (int k = 0; k < K; ++k) dh[k] = dr[k] = x[k] = y[k] = none;
-      if (live) load_row(dh, dr, x, y, r);
-    }
-    open(x, a.r);
-    open(y, a.y);
     // addresses and column tests made anew for each pass over a long row: kept
     // they would take a third of the registers
     if constexpr (K * VEC > 8) asm volatile("" : "+v"(me));
@@ -458,8 +595,8 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
       tbar = q[4] * inv;
       by = a.post ? q[5] * inv : 0.f;
     }
-    const float rx = norm_rstd(q[0] * inv - bx * bx, a.eps);
-    const float ry = a.post ? norm_rstd(q[2] * inv - by * by, a.eps) : 1.f;
+    const float rx = live ? block_rstd(q[0] * inv - bx * bx, a.eps) : 0.f;
+    const float ry = !live ? 0.f : a.post ? block_rstd(q[2] * inv - by * by, a.eps) : 1.f;
     // e = dr + rx t - rx mean(t) - rhat rx mean(t rhat)
     const float c1 = rx * tbar, c2 = rx * (rx * (q[1] * inv - bx * tbar));
     if constexpr (K * VEC > 8) asm volatile("" : "+v"(me));
@@ -484,28 +621,24 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
           float v = C::elem(dr[k], e) + rx * t;
           if constexpr (!RMS) v -= c1;
           ev[k][e] = v - xh * c2;
-          if (live) {
-            b0[k][e] += h;
-            b1[k][e] += h * xh;
-          }
+          b0[k][e] += h;
+          b1[k][e] += h * xh;
         }
       } else {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) ev[k][e] = C::elem(dr[k], e);
       }
-      if (live && col(k) < n) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) out[e] = a.alpha * ev[k][e];
-        C::store(p, col(k), n, out);
-      }
+      for (int e = 0; e < VEC; ++e) out[e] = a.alpha * ev[k][e];
+      IO::store(p, col(k), n, whole(k), live, out);
       if (each) {
         // the gate's own gradient, and the gate into e
         float gate[VEC];
-        load_values<DT>(row_of(a.gate, a.wide_gate, live ? r : 0, a.ldg, E), a.wide_gate, col(k), n, 1.f, gate);
+        load_values<DT, TINY>(row_of(a.gate, a.wide_gate, live ? r : 0, a.ldg, E), a.wide_gate, col(k), n, whole(k), 1.f, gate);
         if (a.dgate && live && col(k) < n) {
           float pg[VEC], pb[VEC];
-          load_values<DT>(a.post ? a.post_gamma : nullptr, a.wide_params, col(k), n, 1.f, pg);
-          load_values<DT>(a.post ? a.post_beta : nullptr, a.wide_params, col(k), n, 0.f, pb);
+          load_values<DT, TINY>(a.post ? a.post_gamma : nullptr, a.wide_params, col(k), n, whole(k), 1.f, pg);
+          load_values<DT, TINY>(a.post ? a.post_beta : nullptr, a.wide_params, col(k), n, whole(k), 0.f, pb);
 #pragma unroll
           for (int e = 0; e < VEC; ++e) {
             const float yh = ((C::elem(y[k], e) - my) - by) * ry;
@@ -535,7 +668,6 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
     }
     if (a.post) meet<W, RMS ? 1 : 2>(s, buf, turn, wave, W * grp);
     keep_packed(y);
-    if (!live) continue;
     // dy = ry s - ry mean(s) - yhat ry mean(s yhat)
     float s1 = 0.f, s2 = 0.f;
     if (a.post) {
@@ -557,8 +689,20 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
         e0[k][e] += v;
         e1[k][e] += v * yh;
       }
-      if (col(k) < n) C::store(p, col(k), n, out);
+      IO::store(p, col(k), n, whole(k), live, out);
     }
+  };
+  // every wave takes as many turns as the workgroup's first row needs
+  int first = begin + slice * GROUPS;
+  if constexpr (AHEAD) {
+    for (; first < end; first += step, r += step) {
+      body(rows[0], rows[1]);
+      first += step, r += step;
+      if (first >= end) break;
+      body(rows[1], rows[0]);
+    }
+  } else {
+    for (; first < end; first += step, r += step) body(rows[0], rows[0]);
   }
   if (!a.part) return;
   float* mine = a.part + (int64_t)blockIdx.x * 4 * n;

@@ -59,8 +59,8 @@ BlockCut block_norm_cut(int64_t rows, int64_t cols, int64_t span, int dt);
 hipError_t launch_block_norm(const BlockNormArgs& a, int dt, hipStream_t s);
 hipError_t launch_block_norm_bwd(const BlockNormArgs& a, const BlockParamsArgs& q, int dt, hipStream_t s);
 
-// One unit to a type (kern_blocknorm_bwd_*.hip).
-template <int DT>
+// One unit to a type and a form of the saved rows (kern_blocknorm_bwd_*.hip).
+template <int DT, bool BYTES>
 hipError_t launch_block_norm_rows(const BlockNormArgs& a, int64_t groups, hipStream_t s);
 
 }  // namespace trt

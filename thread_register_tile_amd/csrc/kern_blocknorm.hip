@@ -30,17 +30,24 @@ hipError_t launch_block_norm(const BlockNormArgs& a, int dt, hipStream_t s) {
       constexpr int THREADS = NormShape<W>::THREADS;
       const int64_t need = (a.rows + NormShape<W>::GROUPS - 1) / NormShape<W>::GROUPS;
       const dim3 grid(even_grid(need, forward_units<W>())), block(THREADS);
-      if (a.gate && a.span == 1) return launch(block_norm_kernel<DT, W, K, true>, grid, block, 0, s, a);
-      return launch(block_norm_kernel<DT, W, K, false>, grid, block, 0, s, a);
+      auto run = [&]<bool TINY>() {
+        if (a.gate && a.span == 1) return launch(block_norm_kernel<DT, W, K, true, TINY>, grid, block, 0, s, a);
+        return launch(block_norm_kernel<DT, W, K, false, TINY>, grid, block, 0, s, a);
+      };
+      if constexpr (K == 1)
+        if (a.cols < RowChunk<DT>::VEC) return run.template operator()<true>();
+      return run.template operator()<false>();
     });
   });
 }
 
 hipError_t launch_block_norm_bwd(const BlockNormArgs& a, const BlockParamsArgs& q, int dt, hipStream_t s) {
   const int64_t groups = q.groups;
-  const hipError_t e = dt == DT_F16    ? launch_block_norm_rows<DT_F16>(a, groups, s)
-                       : dt == DT_BF16 ? launch_block_norm_rows<DT_BF16>(a, groups, s)
-                                       : launch_block_norm_rows<DT_F32>(a, groups, s);
+  const bool bytes = a.y.scale != nullptr;
+  hipError_t e;
+  if (dt == DT_F16) e = bytes ? launch_block_norm_rows<DT_F16, true>(a, groups, s) : launch_block_norm_rows<DT_F16, false>(a, groups, s);
+  else if (dt == DT_BF16) e = bytes ? launch_block_norm_rows<DT_BF16, true>(a, groups, s) : launch_block_norm_rows<DT_BF16, false>(a, groups, s);
+  else e = bytes ? launch_block_norm_rows<DT_F32, true>(a, groups, s) : launch_block_norm_rows<DT_F32, false>(a, groups, s);
   if (e != hipSuccess || !a.part) return e;
   // gate rows: a workgroup's 16 waves take one each, or share one of many slices
   int64_t gates = 0;

@@ -1,9 +1,9 @@
-// kern_blocknorm_bwd_f32.hip -- the block norm's backward kernel for one type of
-// rows, in a translation unit of its own.
+// kern_blocknorm_bwd_f32.hip -- the block norm's backward kernel for one type of rows,
+// in a translation unit of its own.
 #include "kern_blocknorm_bwd.hpp"
 
 namespace trt {
 
-template hipError_t launch_block_norm_rows<DT_F32>(const BlockNormArgs&, int64_t, hipStream_t);
+template hipError_t launch_block_norm_rows<DT_F32, false>(const BlockNormArgs&, int64_t, hipStream_t);
 
 }  // namespace trt

@@ -132,6 +132,7 @@ trt_status trt_block_norm_bwd(int64_t rows, int64_t cols, const void* dh, int64_
   if (!grads || !y || !y->x || !dr || !dy) return fail(TRT_ERR_NULL, "y, dr, dy and grads must be non-null");
   if (!dh && !dr_out) return fail(TRT_ERR_NULL, "dh or dr_out must be non-null");
   if (dh && (!r_out || !r_out->x)) return fail(TRT_ERR_NULL, "dh needs r_out");
+  if (dh && !r_out->scale != !y->scale) return fail(TRT_ERR_ARG, "r_out and y must both be 8-bit rows, or neither");
   const trt_block_grads& g = *grads;
   if (!dh && (g.gamma || g.beta)) return fail(TRT_ERR_NULL, "dgamma and dbeta need dh");
   if (!block->gate && g.gate) return fail(TRT_ERR_NULL, "dgate needs the gate");
