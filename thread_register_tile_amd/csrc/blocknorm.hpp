@@ -241,8 +241,8 @@ __device__ __forceinline__ void meet(float (&v)[N], float (*buf)[128], int& turn
   }
 }
 
-// EACH: a gate of its own for every row, loaded with it; otherwise gate and
-// post norm's parameters are one product, made again when the gate row changes.
+// EACH: gate rows of few rows, loaded with each of them; otherwise a workgroup's
+// rows lie in one gate row, and gate and post norm's parameters are one product.
 // KEEP: the vectors stay in registers (of 16 waves to a row none are left).
 template <int DT, int W, int K, bool EACH, bool TINY>
 __global__ __launch_bounds__(NormShape<W>::THREADS) void block_norm_kernel(BlockNormArgs a) {
@@ -257,9 +257,12 @@ __global__ __launch_bounds__(NormShape<W>::THREADS) void block_norm_kernel(Block
   const int me = 64 * wave + (threadIdx.x & 63);
   const int n = a.cols;
   const float inv = 1.f / (float)a.cols;
-  // a row of workgroups at a time, each of which has a row in every turn
-  const int step = gridDim.x * GROUPS;
-  int r = blockIdx.x * GROUPS + grp;
+  // the workgroup's rows: every `slices`-th GROUPS of one gate row's
+  const int gate_row = blockIdx.x / (uint32_t)a.slices, slice = blockIdx.x % (uint32_t)a.slices;
+  const int begin = EACH ? 0 : gate_row * a.span;
+  const int end = EACH || a.rows - begin < a.span ? a.rows : begin + a.span;
+  const int step = a.slices * GROUPS;
+  int r = begin + slice * GROUPS + grp;
   int turn = 0;
 
   auto col = [&](int k) { return VEC * (me + k * LANES); };
@@ -267,7 +270,7 @@ __global__ __launch_bounds__(NormShape<W>::THREADS) void block_norm_kernel(Block
 
   // u1 yhat + u0 is what the gate multiplies (EACH) or what joins the stream
   float u1[KEEP ? K : 1][VEC], u0[KEEP ? K : 1][VEC], gamma[KEEP ? K : 1][VEC], beta[KEEP ? K : 1][VEC];
-  auto post = [&](int k, int to, int64_t gate_row) {
+  auto post = [&](int k, int to) {
     load_values<DT, TINY>(a.post ? a.post_gamma : nullptr, a.wide_params, col(k), n, whole(k), 1.f, u1[to]);
     load_values<DT, TINY>(a.post ? a.post_beta : nullptr, a.wide_params, col(k), n, whole(k), 0.f, u0[to]);
     if (!EACH && a.gate) {
@@ -288,7 +291,7 @@ __global__ __launch_bounds__(NormShape<W>::THREADS) void block_norm_kernel(Block
   };
   Row rows[2];
   auto load_row = [&](Row& q, int row) __attribute__((always_inline)) {
-    row = row < a.rows ? row : a.rows - 1;
+    row = row < end ? row : end - 1;
     const char *x = row_of(a.r.x, false, row, a.r.ld, E), *y = row_of(a.y.x, false, row, a.y.ld, E);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -299,27 +302,19 @@ __global__ __launch_bounds__(NormShape<W>::THREADS) void block_norm_kernel(Block
   load_row(rows[0], r);
   if constexpr (KEEP)
 #pragma unroll
-    for (int k = 0; k < K; ++k) pre(k, k);
-  int64_t gate_row = -1;
+    for (int k = 0; k < K; ++k) pre(k, k), post(k, k);
   auto body = [&](Row& row, Row& next) __attribute__((always_inline)) {
     auto &x = row.x, &y = row.y;
     float g[EACH ? K : 1][VEC];
+    const int at = (uint32_t)r / (uint32_t)a.span;
     if constexpr (EACH)
 #pragma unroll
       for (int k = 0; k < K; ++k)
-        load_values<DT, TINY>(row_of(a.gate, a.wide_gate, r, a.ldg, E), a.wide_gate, col(k), n, whole(k), 1.f, g[k]);
+        load_values<DT, TINY>(row_of(a.gate, a.wide_gate, at, a.ldg, E), a.wide_gate, col(k), n, whole(k), 1.f, g[k]);
     load_row(next, r + step);
 #pragma unroll
     for (int k = 0; k < K; ++k)
       if (!whole(k)) x[k] = IO::fix(x[k], col(k), n), y[k] = IO::fix(y[k], col(k), n);
-    const int64_t at = EACH ? 0 : (int64_t)((uint32_t)r / (uint32_t)a.span);
-    if constexpr (KEEP)
-      if (at != gate_row) {
-#pragma unroll
-        for (int k = 0; k < K; ++k) post(k, k, at);
-      }
-    gate_row = at;
-
     float m = 0.f, dbar = 0.f, rstd = 1.f;
     if (a.post) {
       if (!a.rms) {
@@ -352,7 +347,7 @@ __global__ __launch_bounds__(NormShape<W>::THREADS) void block_norm_kernel(Block
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int to = KEEP ? k : 0;
-      if constexpr (!KEEP) post(k, 0, at);
+      if constexpr (!KEEP) post(k, 0);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) z[k][e] = 0.f;
       for_elems<VEC>(n - col(k), [&](int e) {
@@ -391,10 +386,10 @@ __global__ __launch_bounds__(NormShape<W>::THREADS) void block_norm_kernel(Block
       IO::store(p, col(k), n, whole(k), a.out_y, h);
     }
   };
-  for (; r < a.rows; r += step) {
+  for (; r < end; r += step) {
     body(rows[0], rows[1]);
     r += step;
-    if (r >= a.rows) break;
+    if (r >= end) break;
     body(rows[1], rows[0]);
   }
 }

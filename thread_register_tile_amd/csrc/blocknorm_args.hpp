@@ -31,7 +31,7 @@ struct BlockNormArgs {
   void* dgate;           // a gate of its own for every row: written with dr and dy
   int64_t lddg;
   float* part;           // [groups * slices][4][cols] sums of e, e yhat, dh, dh rhat; or null
-  int32_t slices;        // workgroups to a gate row
+  int32_t slices;        // workgroups to a gate row (both passes)
 };
 
 // The parameters' and the gate rows' gradients from the workgroups' sums.
@@ -56,7 +56,7 @@ struct BlockCut {
 };
 BlockCut block_norm_cut(int64_t rows, int64_t cols, int64_t span, int dt);
 
-hipError_t launch_block_norm(const BlockNormArgs& a, int dt, hipStream_t s);
+hipError_t launch_block_norm(BlockNormArgs a, int dt, hipStream_t s);   // (a.slices: its own choice)
 hipError_t launch_block_norm_bwd(const BlockNormArgs& a, const BlockParamsArgs& q, int dt, hipStream_t s);
 
 // One unit to a type and a form of the saved rows (kern_blocknorm_bwd_*.hip).

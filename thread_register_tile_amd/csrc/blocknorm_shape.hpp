@@ -10,19 +10,35 @@ constexpr int64_t block_chunks(int64_t cols, int dt) {
   return dt == DT_F32 ? (cols + 3) / 4 : (cols + 7) / 8;
 }
 
-// W waves to a row, K 16-byte chunks to a lane: two chunks, so that the vectors
-// a lane keeps and the sums of the backward pass fit beside the rows, and as few
-// waves as hold the row.  f is called with <W, K>.
+// W waves to a row, K 16-byte chunks to a lane, as few waves as hold the row.  f
+// is called with <W, K>.
+template <int K, class F>
+auto with_row_waves(int64_t chunks, F&& f) {
+  const int64_t waves = (chunks + 64 * K - 1) / (64 * K);
+  if (waves <= 1) return f.template operator()<1, K>();
+  if (waves <= 2) return f.template operator()<2, K>();
+  if (waves <= 4) return f.template operator()<4, K>();
+  if (waves <= 6) return f.template operator()<6, K>();
+  if (waves <= 8) return f.template operator()<8, K>();
+  if (waves <= 12) return f.template operator()<12, K>();
+  return f.template operator()<16, K>();
+}
+
+// Forward: one chunk, two from 768 on (16384 rows of 1024 chunks 190 us in 8
+// waves of two, 207 in 16 of one; 4000 rows of 625 52 and 36).
 template <class F>
-auto with_block_shape(int64_t chunks, F&& f) {
-  if (chunks <= 64) return f.template operator()<1, 1>();
-  if (chunks <= 128) return f.template operator()<1, 2>();
-  if (chunks <= 256) return f.template operator()<2, 2>();
-  if (chunks <= 512) return f.template operator()<4, 2>();
-  if (chunks <= 768) return f.template operator()<6, 2>();
+auto with_forward_shape(int64_t chunks, F&& f) {
+  if (chunks <= 768) return with_row_waves<1>(chunks, f);
   if (chunks <= 1024) return f.template operator()<8, 2>();
   if (chunks <= 1536) return f.template operator()<12, 2>();
   return f.template operator()<16, 2>();
+}
+
+// Backward: two chunks, so that the vectors and sums that a lane keeps fit beside
+// the rows.
+template <class F>
+auto with_block_shape(int64_t chunks, F&& f) {
+  return chunks <= 64 ? f.template operator()<1, 1>() : with_row_waves<2>(chunks, f);
 }
 
 // Workgroups for `need` turns, at most `most`, each with the same number of
@@ -32,11 +48,24 @@ constexpr int64_t even_grid(int64_t need, int64_t most) {
   return (need + turns - 1) / turns;
 }
 
+// Slices of a gate row of `need` turns, where `most` workgroups run at a time: the
+// number that takes the least turns, counting a round's start and end as `beside`.
+inline int64_t cheapest_slices(int64_t need, int64_t groups, int64_t most, int64_t beside) {
+  if (groups == 1) return even_grid(need, most);
+  int64_t best = 1, least = -1;
+  for (int64_t s = 1; s <= need && (s == 1 || s * groups <= 4 * most); ++s) {
+    const int64_t cost = (s * groups + most - 1) / most * ((need + s - 1) / s + beside);
+    if (least < 0 || cost < least) best = s, least = cost;
+  }
+  return best;
+}
+
 // Forward workgroups, 16 waves to each of the 256 units (a row's own where it
 // has more).
 template <int W>
-constexpr int64_t forward_units() {
-  return 256 * (16 / (NormShape<W>::THREADS / 64) > 0 ? 16 / (NormShape<W>::THREADS / 64) : 1);
+int64_t forward_slices(int64_t span, int64_t groups) {
+  constexpr int waves = NormShape<W>::THREADS / 64, each = 16 / waves > 0 ? 16 / waves : 1;
+  return cheapest_slices((span + NormShape<W>::GROUPS - 1) / NormShape<W>::GROUPS, groups, 256 * each, 1);
 }
 
 // Backward workgroups: 8 waves, of which a row has W (and as many as it needs
@@ -53,20 +82,12 @@ bool block_large(int64_t rows) {
   return kBlockWaves<W> != kBlockFewWaves<W> && (rows + per - 1) / per >= 256;
 }
 
-// Slices of a gate row of `span` rows: the number that takes the least turns
-// where one workgroup runs on a unit at a time, counting a round of starting and
-// ending (the sums' store) as two turns.
+// Slices of a gate row of `span` rows; one workgroup runs on a unit at a time, and
+// its end is the store of four sums.
 inline int64_t block_slices(int64_t rows, int64_t span, int64_t groups, int64_t chunks) {
   return with_block_shape(chunks, [&]<int W, int K>() -> int64_t {
     const int64_t per = (block_large<W>(rows) ? kBlockWaves<W> : kBlockFewWaves<W>) / W;
-    const int64_t need = ((span < rows ? span : rows) + per - 1) / per;
-    if (groups == 1) return even_grid(need, 256);
-    int64_t best = 1, least = -1;
-    for (int64_t s = 1; s <= need && (s == 1 || s * groups <= 1024); ++s) {
-      const int64_t cost = (s * groups + 255) / 256 * ((need + s - 1) / s + 2);
-      if (least < 0 || cost < least) best = s, least = cost;
-    }
-    return best;
+    return cheapest_slices(((span < rows ? span : rows) + per - 1) / per, groups, 256, 2);
   });
 }
 

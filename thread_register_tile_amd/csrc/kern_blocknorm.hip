@@ -24,17 +24,20 @@ BlockCut block_norm_cut(int64_t rows, int64_t cols, int64_t span, int dt) {
   return {groups, block_slices(rows, span, groups, block_chunks(cols, dt))};
 }
 
-hipError_t launch_block_norm(const BlockNormArgs& a, int dt, hipStream_t s) {
+hipError_t launch_block_norm(BlockNormArgs a, int dt, hipStream_t s) {
+  // a gate row of few rows is read with each of them: as workgroups of their own
+  // they would start for a few turns only
+  const bool each = a.gate && (a.span <= 8 || a.rows / a.span >= 1 << 20);
+  const int64_t span = each ? a.rows : a.span, groups = (a.rows + span - 1) / span;
   return with_type(dt, [&]<int DT>() {
-    return with_block_shape(block_chunks(a.cols, DT), [&]<int W, int K>() {
-      constexpr int THREADS = NormShape<W>::THREADS;
-      const int64_t need = (a.rows + NormShape<W>::GROUPS - 1) / NormShape<W>::GROUPS;
-      const dim3 grid(even_grid(need, forward_units<W>())), block(THREADS);
+    return with_forward_shape(block_chunks(a.cols, DT), [&]<int W, int K>() {
+      a.slices = (int32_t)forward_slices<W>(span, groups);
+      const dim3 grid(groups * a.slices), block(NormShape<W>::THREADS);
       auto run = [&]<bool TINY>() {
-        if (a.gate && a.span == 1) return launch(block_norm_kernel<DT, W, K, true, TINY>, grid, block, 0, s, a);
+        if (each) return launch(block_norm_kernel<DT, W, K, true, TINY>, grid, block, 0, s, a);
         return launch(block_norm_kernel<DT, W, K, false, TINY>, grid, block, 0, s, a);
       };
-      if constexpr (K == 1)
+      if constexpr (W == 1 && K == 1)
         if (a.cols < RowChunk<DT>::VEC) return run.template operator()<true>();
       return run.template operator()<false>();
     });

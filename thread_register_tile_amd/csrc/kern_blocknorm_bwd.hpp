@@ -19,7 +19,7 @@ hipError_t launch_block_norm_rows(const BlockNormArgs& a, int64_t groups, hipStr
                    : launch(block_norm_bwd_kernel<DT, BYTES, W, K, WAVES, false, TINY>, grid, block, 0, s, a);
     };
     const bool large = block_large<W>(a.rows);
-    if constexpr (K == 1)
+    if constexpr (W == 1 && K == 1)
       if (a.cols < RowChunk<DT>::VEC)
         return large ? run.template operator()<MANY, true>() : run.template operator()<FEW, true>();
     return large ? run.template operator()<MANY, false>() : run.template operator()<FEW, false>();
