@@ -311,21 +311,33 @@ def layout_dump_host(map_id, tile):
 
 # ---- torch-facing helpers (device memory and the current stream) ----------------
 
+_TORCH = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
 
 
 _DT = {}
 
 
-def _dtype_code(t):
-    torch = _torch()
-    if not _DT:
+def _code_of(dtype):
+    code = _DT.get(dtype)
+    if code is None:
+        torch = _torch()
         _DT.update({torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32})
-    if t.dtype not in _DT:
-        raise TrtError(ERR_DTYPE, f"unsupported dtype {t.dtype}")
-    return _DT[t.dtype]
+        if dtype not in _DT:
+            raise TrtError(ERR_DTYPE, f"unsupported dtype {dtype}")
+        code = _DT[dtype]
+    return code
+
+
+def _dtype_code(t):
+    return _code_of(t.dtype)
 
 
 def _stream(device):
@@ -624,6 +636,17 @@ def _device(first, **others):
     return dev
 
 
+def _place(first, *others):
+    """_device for calls of many small tensors: the device that all of them live on."""
+    index = first.get_device()
+    if index < 0:
+        raise TrtError(ERR_ARG, "tensors must be on a GPU")
+    for t in others:
+        if t is not None and t.get_device() != index:
+            raise TrtError(ERR_ARG, f"a tensor is on {t.device}, not on {first.device}")
+    return first.device
+
+
 def _on(dev, status_of):
     """status_of(stream) with dev current (a launch goes to the current device)."""
     torch = _torch()
@@ -647,19 +670,24 @@ def _rows(t, name):
             t = t.view(-1, t.size(-1))
         except RuntimeError:
             raise TrtError(ERR_STRIDE, f"{name} does not view as rows of its last dimension") from None
-    rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    (rows, cols), (ld, inner) = t.shape, t.stride()
+    if cols > 1 and inner != 1:
         raise TrtError(ERR_STRIDE, f"{name} must have unit inner stride")
-    if rows > 1 and t.stride(0) < 1:
+    if rows > 1 and ld < 1:
         raise TrtError(ERR_STRIDE, f"{name}: rows must have a positive stride")
-    return rows, cols, t.stride(0) if rows > 1 else max(cols, 1)
+    return rows, cols, ld if rows > 1 else max(cols, 1)
+
+
+def _ld_as(t, name, like, ld):
+    """The leading dimension of t, of `like`'s shape, whose own is ld."""
+    return ld if t.stride() == like.stride() else _rows(t, name)[2]
 
 
 def _vector(t, name, n, dtype):
     """Address of a contiguous vector of n elements of dtype, or None."""
     if t is None:
         return None
-    if t.dim() != 1 or t.numel() != n or (n > 1 and t.stride(0) != 1):
+    if t.dim() != 1 or t.size(0) != n or not t.is_contiguous():
         raise TrtError(ERR_SIZE, f"{name} must be contiguous with {n} elements")
     if t.dtype != dtype:
         raise TrtError(ERR_DTYPE, f"{name} must be {dtype}")
@@ -674,6 +702,14 @@ def _like(out, t, name):
     if out.shape != t.shape or out.dtype != t.dtype:
         raise TrtError(ERR_SIZE, f"{name} must be {list(t.shape)} of {t.dtype}")
     return out
+
+
+def _new(t, dtype=None):
+    """A new contiguous tensor of t's shape, of dtype or t's."""
+    empty_like = _torch().empty_like
+    if t.is_contiguous():
+        return empty_like(t, dtype=dtype) if dtype else empty_like(t)
+    return empty_like(t, dtype=dtype, memory_format=_torch().contiguous_format)
 
 
 def _workspace(ws, need, like):
@@ -895,9 +931,9 @@ def _act8(q, scale, name=""):
     if q.dtype != torch.int8 or scale.dtype != torch.uint8:
         raise TrtError(ERR_DTYPE, f"{name}q must be int8 and {name}scale uint8")
     rows, cols, ldq = _rows(q, f"{name}q")
-    blocks = -(-cols // ACT8_BLOCK)
-    if scale.dim() != q.dim() or scale.shape[:-1] != q.shape[:-1] or scale.size(-1) != blocks:
-        raise TrtError(ERR_SIZE, f"{name}scale must be {[*q.shape[:-1], blocks]}")
+    want = (*q.shape[:-1], -(-cols // ACT8_BLOCK))
+    if scale.shape != want:
+        raise TrtError(ERR_SIZE, f"{name}scale must be {list(want)}")
     return rows, cols, ldq, _rows(scale, f"{name}scale")[2]
 
 
@@ -911,14 +947,17 @@ def act8_pack(x, *, q=None, scale=None):
     """
     torch = _torch()
     rows, cols, ldx = _rows(x, "x")
+    ldq, lds = max(cols, 1), max(-(-cols // ACT8_BLOCK), 1)
+    given = q is not None or scale is not None
     if q is None:
-        q = torch.empty_like(x, dtype=torch.int8, memory_format=torch.contiguous_format)
+        q = _new(x, torch.int8)
     elif q.shape != x.shape:
         raise TrtError(ERR_SIZE, f"q must be {list(x.shape)}")
     if scale is None:
         scale = x.new_empty((*x.shape[:-1], -(-cols // ACT8_BLOCK)), dtype=torch.uint8)
-    _, _, ldq, lds = _act8(q, scale)
-    dev = _device(x, q=q, scale=scale)
+    if given:
+        _, _, ldq, lds = _act8(q, scale)
+    dev = _place(x, q, scale)
     _on(dev, lambda s: lib().trt_act8_pack(rows, cols, x.data_ptr(), ldx, q.data_ptr(), ldq, scale.data_ptr(), lds,
                                            _dtype_code(x), s))
     return q, scale
@@ -930,16 +969,16 @@ def act8_unpack(q, scale, dtype, *, out=None):
     if given, has q's shape and dtype; otherwise a new tensor is returned.  Runs
     on torch's current stream; no synchronisation.
     """
-    torch = _torch()
     rows, cols, ldq, lds = _act8(q, scale)
     if out is None:
-        out = torch.empty_like(q, dtype=dtype, memory_format=torch.contiguous_format)
+        out, ldx = _new(q, dtype), max(cols, 1)
     elif out.shape != q.shape or out.dtype != dtype:
         raise TrtError(ERR_SIZE, f"out must be {list(q.shape)} of {dtype}")
-    ldx = _rows(out, "out")[2]
-    dev = _device(q, scale=scale, out=out)
+    else:
+        ldx = _rows(out, "out")[2]
+    dev = _place(q, scale, out)
     _on(dev, lambda s: lib().trt_act8_unpack(rows, cols, q.data_ptr(), ldq, scale.data_ptr(), lds, out.data_ptr(),
-                                             ldx, _dtype_code(out), s))
+                                             ldx, _code_of(dtype), s))
     return out
 
 
@@ -962,17 +1001,19 @@ def act8_weight_grad(dy, q, scale, *, out_dtype=None, dw=None, workspace=None):
     allocated.  Runs on torch's current stream; no synchronisation.
     """
     tokens, inputs, ldq, lds = _act8(q, scale)
-    rows, outputs, lddy = _rows(dy, "dy")
+    _, outputs, lddy = _rows(dy, "dy")
     if dy.shape[:-1] != q.shape[:-1]:
         raise TrtError(ERR_SIZE, f"dy must have q's leading shape {list(q.shape[:-1])}")
     if dw is None:
-        dw = dy.new_empty((outputs, inputs), dtype=out_dtype or dy.dtype)
+        dw, lddw = dy.new_empty((outputs, inputs), dtype=out_dtype or dy.dtype), max(inputs, 1)
     elif dw.dim() != 2 or dw.shape != (outputs, inputs) or dw.dtype != (out_dtype or dw.dtype):
         raise TrtError(ERR_SIZE, f"dw must be [{outputs}, {inputs}] of {out_dtype or dw.dtype}")
-    lddw = _rows(dw, "dw")[2]
-    workspace = _workspace(workspace, act8_weight_grad_workspace_size(tokens, outputs, inputs, dy.data_ptr(), lddy), dy)
-    dev = _device(dy, q=q, scale=scale, dw=dw, workspace=workspace)
-    _on(dev, lambda s: lib().trt_act8_weight_grad(tokens, outputs, inputs, dy.data_ptr(), lddy, q.data_ptr(), ldq,
+    else:
+        lddw = _rows(dw, "dw")[2]
+    at = dy.data_ptr()
+    workspace = _workspace(workspace, act8_weight_grad_workspace_size(tokens, outputs, inputs, at, lddy), dy)
+    dev = _place(dy, q, scale, dw, workspace)
+    _on(dev, lambda s: lib().trt_act8_weight_grad(tokens, outputs, inputs, at, lddy, q.data_ptr(), ldq,
                                                   scale.data_ptr(), lds, dw.data_ptr(), lddw, _dtype_code(dy),
                                                   _dtype_code(dw), workspace.data_ptr(), workspace.nbytes, s))
     return dw
@@ -1000,30 +1041,25 @@ def _gate_span(gate, shape, rows, cols, rows_per_gate):
     return span
 
 
-def _block(x, gate, post, post_gamma, post_beta, gamma, beta, alpha, rms, eps, rows_per_gate):
-    """(Block, gate's span or 0, parameters' dtype) for rows of x."""
-    rows, cols, _ = _rows(x, "x")
-    param = next((t.dtype for t in (post_gamma, post_beta, gamma, beta) if t is not None), x.dtype)
-    b = Block()
-    b.post_gamma, b.post_beta = _vector(post_gamma, "post_gamma", cols, param), _vector(post_beta, "post_beta", cols, param)
-    b.gamma, b.beta = _vector(gamma, "gamma", cols, param), _vector(beta, "beta", cols, param)
-    b.alpha, b.eps, b.post, b.rms = alpha, eps, int(post), int(rms)
-    b.param_dtype = _dtype_code(x) if param is x.dtype else _code_of(param)
-    span = 0
+def _block(x, rows, cols, gate, post, post_gamma, post_beta, gamma, beta, alpha, rms, eps, rows_per_gate, none):
+    """(Block, gate's span or 0, parameters' dtype) for rows of x; none: the
+    parameters' dtype where none is given."""
+    param = none
+    for t in (post_gamma, post_beta, gamma, beta):
+        if t is not None:
+            param = t.dtype
+            break
+    span = at = ldg = 0
+    gate_code = F32
     if gate is not None:
         span = _gate_span(gate, x.shape, rows, cols, rows_per_gate)
-        b.gate, b.ldg, b.rows_per_gate, b.gate_dtype = gate.data_ptr(), _rows(gate, "gate")[2], span, _dtype_code(gate)
+        at, ldg, gate_code = gate.data_ptr(), cols if gate.is_contiguous() else _rows(gate, "gate")[2], _code_of(gate.dtype)
     elif rows_per_gate is not None:
         raise TrtError(ERR_ARG, "rows_per_gate without a gate")
-    return b, span, param
-
-
-def _code_of(dtype):
-    torch = _torch()
-    codes = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
-    if dtype not in codes:
-        raise TrtError(ERR_DTYPE, f"unsupported dtype {dtype}")
-    return codes[dtype]
+    return Block(at or None, ldg, span, _vector(post_gamma, "post_gamma", cols, param),
+                 _vector(post_beta, "post_beta", cols, param), _vector(gamma, "gamma", cols, param),
+                 _vector(beta, "beta", cols, param), alpha, eps, bool(post), bool(rms), gate_code,
+                 _code_of(param)), span, param
 
 
 def block_norm(r, y, gate=None, *, post=True, post_gamma=None, post_beta=None, gamma=None, beta=None,
@@ -1048,15 +1084,23 @@ def block_norm(r, y, gate=None, *, post=True, post_gamma=None, post_beta=None, g
     if h is not None and not need_h:
         raise TrtError(ERR_ARG, "h given without need_h")
     rows, cols, ldr = _rows(r, "r")
-    block, _, _ = _block(r, gate, post, post_gamma, post_beta, gamma, beta, alpha, rms, eps, rows_per_gate)
-    r_out = _like(r_out, r, "r_out")
-    if need_h:
-        h = _like(h, r, "h")
-    ldro, ldh = _rows(r_out, "r_out")[2], 0 if h is None else _rows(h, "h")[2]
-    dev = _device(r, y=y, gate=gate, post_gamma=post_gamma, post_beta=post_beta, gamma=gamma, beta=beta, r_out=r_out, h=h)
-    _on(dev, lambda s: lib().trt_block_norm(rows, cols, r.data_ptr(), ldr, y.data_ptr(), _rows(y, "y")[2], block,
-                                            r_out.data_ptr(), ldro, None if h is None else h.data_ptr(), ldh,
-                                            _dtype_code(r), s))
+    ldy, ldro = _ld_as(y, "y", r, ldr), max(cols, 1)
+    ldh = ldro
+    block, _, _ = _block(r, rows, cols, gate, post, post_gamma, post_beta, gamma, beta, alpha, rms, eps, rows_per_gate, r.dtype)
+    if r_out is None:
+        r_out = _new(r)
+    else:
+        ldro = _rows(_like(r_out, r, "r_out"), "r_out")[2]
+    if not need_h:
+        h_at = None
+    elif h is None:
+        h = _new(r)
+        h_at = h.data_ptr()
+    else:
+        ldh, h_at = _rows(_like(h, r, "h"), "h")[2], h.data_ptr()
+    dev = _place(r, y, gate, post_gamma, post_beta, gamma, beta, r_out, h)
+    _on(dev, lambda s: lib().trt_block_norm(rows, cols, r.data_ptr(), ldr, y.data_ptr(), ldy, block, r_out.data_ptr(),
+                                            ldro, h_at, ldh, _dtype_code(r), s))
     return r_out, h
 
 
@@ -1069,17 +1113,17 @@ def block_norm_bwd_workspace_size(rows, cols, rows_per_gate=0, dtype=F16) -> int
     return n
 
 
-def _saved(t, name, shape, dtype):
-    """(Saved, its tensors) of rows of dtype, or of 8-bit ones as (q, scale)."""
+def _saved(t, name, up, ld):
+    """(Saved, its two tensors) of rows like up's, or of 8-bit ones as (q, scale)."""
     if isinstance(t, (tuple, list)):
         q, scale = t
         _, _, ldq, lds = _act8(q, scale, f"{name}'s ")
-        if q.shape != shape:
-            raise TrtError(ERR_SIZE, f"{name}'s q must be {list(shape)}")
-        return Saved(q.data_ptr(), ldq, scale.data_ptr(), lds), {f"{name}'s q": q, f"{name}'s scale": scale}
-    if t.shape != shape or t.dtype != dtype:
-        raise TrtError(ERR_SIZE, f"{name} must be {list(shape)} of {dtype}, or act8_pack's (q, scale) of that shape")
-    return Saved(t.data_ptr(), _rows(t, name)[2], None, 0), {name: t}
+        if q.shape != up.shape:
+            raise TrtError(ERR_SIZE, f"{name}'s q must be {list(up.shape)}")
+        return Saved(q.data_ptr(), ldq, scale.data_ptr(), lds), q, scale
+    if t.shape != up.shape or t.dtype != up.dtype:
+        raise TrtError(ERR_SIZE, f"{name} must be {list(up.shape)} of {up.dtype}, or act8_pack's (q, scale) of that shape")
+    return Saved(t.data_ptr(), _ld_as(t, name, up, ld), None, 0), t, None
 
 
 def block_norm_bwd(dh, dr_out, r_out, y, gate=None, *, post=True, post_gamma=None, post_beta=None, gamma=None,
@@ -1101,44 +1145,50 @@ def block_norm_bwd(dh, dr_out, r_out, y, gate=None, *, post=True, post_gamma=Non
     up = dr_out if dh is None else dh
     if up is None:
         raise TrtError(ERR_NULL, "dh or dr_out must be given")
-    rows, cols, _ = _rows(up, "dh")
+    rows, cols, ld = _rows(up, "dh")
     if dr_out is not None and (dr_out.shape != up.shape or dr_out.dtype != up.dtype):
         raise TrtError(ERR_SIZE, f"dr_out must be {list(up.shape)} of {up.dtype}")
     if dh is not None and r_out is None:
         raise TrtError(ERR_NULL, "dh needs r_out")
-    block, span, param = _block(up, gate, post, post_gamma, post_beta, gamma, None, alpha, rms, eps, rows_per_gate)
-    if gamma is None and post_gamma is None and post_beta is None:
-        param, block.param_dtype = torch.float32, F32
+    block, span, param = _block(up, rows, cols, gate, post, post_gamma, post_beta, gamma, None, alpha, rms, eps, rows_per_gate,
+                                torch.float32)
     code = _dtype_code(up)
-    sy, tensors = _saved(y, "y", up.shape, up.dtype)
-    sr = None
+    sy, y0, y1 = _saved(y, "y", up, ld)
+    sr = r0 = r1 = None
     if dh is not None:
-        sr, more = _saved(r_out, "r_out", up.shape, up.dtype)
-        tensors.update(more)
-    dr, dy = _like(dr, up, "dr"), _like(dy, up, "dy")
-    grads = BlockGrads()
+        sr, r0, r1 = _saved(r_out, "r_out", up, ld)
+    lddr = lddy = max(cols, 1)
+    if dr is None:
+        dr = _new(up)
+    else:
+        lddr = _rows(_like(dr, up, "dr"), "dr")[2]
+    if dy is None:
+        dy = _new(up)
+    else:
+        lddy = _rows(_like(dy, up, "dy"), "dy")[2]
     dgate = dpg = dpb = dg = db = None
     if params:
         if gate is not None:
-            dgate = torch.empty_like(gate, memory_format=torch.contiguous_format)
-            grads.gate, grads.ldg = dgate.data_ptr(), cols
-        made = iter(up.new_empty((2 * post + 2 * (dh is not None), cols), dtype=param))
-        if post:
-            dpg, dpb = next(made), next(made)
-            grads.post_gamma, grads.post_beta = dpg.data_ptr(), dpb.data_ptr()
-        if dh is not None:
-            dg, db = next(made), next(made)
-            grads.gamma, grads.beta = dg.data_ptr(), db.data_ptr()
-        workspace = _workspace(workspace, block_norm_bwd_workspace_size(rows, cols, span, code), up)
+            dgate = _new(gate)
+        made = 2 * bool(post) + 2 * (dh is not None)
+        if made:
+            made = up.new_empty((made, cols), dtype=param).unbind()
+            if post:
+                dpg, dpb = made[:2]
+            if dh is not None:
+                dg, db = made[-2:]
+        need = lib().trt_block_norm_bwd_workspace_size(rows, cols, span, code)
+        if need < 0:
+            raise TrtError(ERR_ARG, last_error())
+        workspace = _workspace(workspace, need, up)
+        ws, wsb = workspace.data_ptr(), workspace.nbytes
     else:
-        workspace = None
-    dev = _device(up, dr_out=dr_out, gate=gate, post_gamma=post_gamma, post_beta=post_beta, gamma=gamma, dr=dr, dy=dy,
-                  workspace=workspace, **tensors)
-    ws, wsb = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
-
-    def ptr(t, name):
-        return (None, 0) if t is None else (t.data_ptr(), _rows(t, name)[2])
-
-    _on(dev, lambda s: lib().trt_block_norm_bwd(rows, cols, *ptr(dh, "dh"), *ptr(dr_out, "dr_out"), sr, sy, block,
-                                                *ptr(dr, "dr"), *ptr(dy, "dy"), grads, code, ws, wsb, s))
+        workspace, ws, wsb = None, None, 0
+    grads = BlockGrads(*((None, 0) if dgate is None else (dgate.data_ptr(), cols)),
+                       *(None if t is None else t.data_ptr() for t in (dpg, dpb, dg, db)))
+    dev = _place(up, dr_out, gate, post_gamma, post_beta, gamma, dr, dy, workspace, y0, y1, r0, r1)
+    dh_at, lddh = (None, 0) if dh is None else (dh.data_ptr(), ld)
+    dr_at, lddro = (None, 0) if dr_out is None else (dr_out.data_ptr(), _ld_as(dr_out, "dr_out", up, ld))
+    _on(dev, lambda s: lib().trt_block_norm_bwd(rows, cols, dh_at, lddh, dr_at, lddro, sr, sy, block, dr.data_ptr(), lddr,
+                                                dy.data_ptr(), lddy, grads, code, ws, wsb, s))
     return dr, dy, dgate, dpg, dpb, dg, db

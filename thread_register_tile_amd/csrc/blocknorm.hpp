@@ -407,11 +407,14 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
   using Q = Act8Chunk<DT>;
   using IO = RowIO<DT, TINY>;
   constexpr int VEC = C::VEC, LANES = 64 * W, GROUPS = WAVES / W, E = sizeof(typename C::Elem);
-  constexpr int ROOM = WAVES <= 8 ? 216 : 0;         // of 256 registers (168 and 128 of 12 and 16 waves)
-  constexpr int HELD = K * (16 + 5 * VEC);           // the rows, e and the sums
+  // of 256, 168 and 128 registers; HELD: the rows, e and the sums
+  constexpr int ROOM = WAVES <= 8 ? 216 : WAVES <= 12 ? 118 : 78;
+  constexpr bool PART = WAVES > 8 && K * VEC > 8;    // dgamma's and dbeta's sums wait in LDS
+  constexpr int HELD = K * (16 + (PART ? 3 : 5) * VEC);
   constexpr bool AHEAD = HELD + 16 * K <= ROOM, KEPT = AHEAD && HELD + 16 * K + 2 * VEC * K <= ROOM;
   __shared__ float buf[2][128];
   __shared__ float fold[GROUPS > 1 ? GROUPS : 1][GROUPS > 1 ? LANES * VEC * K : 1];
+  __shared__ f32x4 kept[2][PART ? K * VEC / 4 : 1][PART ? 64 * WAVES : 1];   // a lane's own entries
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wave = w % W, grp = w / W;
   int me = 64 * wave + (threadIdx.x & 63);
@@ -453,15 +456,20 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
       }
     }
   };
-  auto load_row = [&](Row& q, int row) __attribute__((always_inline)) {
+  auto load_up = [&](Row& q, int row) __attribute__((always_inline)) {
     row = row < end ? row : end - 1;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       q.dh[k] = IO::load(dhp + row * lddh * (int64_t)E, col(k), n);
       q.dr[k] = IO::load(drp + row * lddr * (int64_t)E, col(k), n);
     }
-    load_saved(q.x, q.xb, xs, row);
-    load_saved(q.y, q.yb, ys, row);
+  };
+  auto load_x = [&](Row& q, int row) __attribute__((always_inline)) { load_saved(q.x, q.xb, xs, row < end ? row : end - 1); };
+  auto load_y = [&](Row& q, int row) __attribute__((always_inline)) { load_saved(q.y, q.yb, ys, row < end ? row : end - 1); };
+  auto load_row = [&](Row& q, int row) __attribute__((always_inline)) {
+    load_up(q, row);
+    load_x(q, row);
+    load_y(q, row);
   };
   auto open_saved = [&](u32x4 (&to)[K], const Saved (&v)[K], const uint32_t (&b)[K]) __attribute__((always_inline)) {
 #pragma unroll
@@ -498,9 +506,10 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
 #pragma unroll
     for (int e = 0; e < VEC; ++e) v[e] *= g[e];
   };
-  // two rows' registers, used in turn: the one at work and the one on its way
+  // two rows' registers, used in turn: the one at work and the one on its way; or
+  // one, each part of which is loaded again as soon as it has been used
   Row rows[AHEAD ? 2 : 1];
-  if constexpr (AHEAD) load_row(rows[0], r);
+  load_row(rows[0], r);
   if constexpr (KEPT)
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -508,23 +517,30 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
       get_post(k, gp[k]);
     }
 
-  float e0[K][VEC], e1[K][VEC], b0[K][VEC], b1[K][VEC];
+  float e0[K][VEC], e1[K][VEC], b0[PART ? 1 : K][VEC], b1[PART ? 1 : K][VEC];
 #pragma unroll
   for (int k = 0; k < K; ++k)
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) e0[k][e] = e1[k][e] = b0[k][e] = b1[k][e] = 0.f;
+    for (int e = 0; e < VEC; ++e) e0[k][e] = e1[k][e] = b0[PART ? 0 : k][e] = b1[PART ? 0 : k][e] = 0.f;
+  if constexpr (PART)
+#pragma unroll
+    for (int v = 0; v < K * VEC / 4; ++v) kept[0][v][threadIdx.x] = kept[1][v][threadIdx.x] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   // One row; a wave whose row lies past the end works on zeros, with rstd = 0, and
   // stores nothing.
   auto body = [&](Row& row, Row& next) __attribute__((always_inline)) {
     const bool live = GROUPS == 1 || r < end;
-    load_row(AHEAD ? next : row, AHEAD ? r + step : r);
+    if constexpr (AHEAD) load_row(next, r + step);
     u32x4 (&dh)[K] = row.dh, (&dr)[K] = row.dr, x[K], y[K];
 #pragma unroll
     for (int k = 0; k < K; ++k)
       if (!whole(k)) dh[k] = IO::fix(dh[k], col(k), n), dr[k] = IO::fix(dr[k], col(k), n);
     open_saved(x, row.x, row.xb);
     open_saved(y, row.y, row.yb);
+    if constexpr (!AHEAD && BYTES) {
+      load_x(row, r + step);
+      load_y(row, r + step);
+    }
     if (!a.dr)
 #pragma unroll
       for (int k = 0; k < K; ++k) dr[k] = none;
@@ -608,6 +624,7 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
         get_post(k, pm);
       }
       float out[VEC];
+      f32x4 part[2];
       if (a.dh) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
@@ -616,8 +633,16 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
           float v = C::elem(dr[k], e) + rx * t;
           if constexpr (!RMS) v -= c1;
           ev[k][e] = v - xh * c2;
-          b0[k][e] += h;
-          b1[k][e] += h * xh;
+          if constexpr (!PART) {
+            b0[k][e] += h;
+            b1[k][e] += h * xh;
+          } else {
+            // (one after the other: four sums at a time go through registers)
+            if (e % 4 == 0) part[0] = kept[0][(VEC * k + e) / 4][threadIdx.x], part[1] = kept[1][(VEC * k + e) / 4][threadIdx.x];
+            part[0][e % 4] += h;
+            part[1][e % 4] += h * xh;
+            if (e % 4 == 3) kept[0][(VEC * k + e) / 4][threadIdx.x] = part[0], kept[1][(VEC * k + e) / 4][threadIdx.x] = part[1];
+          }
         }
       } else {
 #pragma unroll
@@ -661,6 +686,10 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
         if constexpr (!RMS) s[1] += sv;
       }
     }
+    if constexpr (!AHEAD) {
+      load_up(row, r + step);
+      if constexpr (!BYTES) load_x(row, r + step);
+    }
     if (a.post) meet<W, RMS ? 1 : 2>(s, buf, turn, wave, W * grp);
     keep_packed(y);
     // dy = ry s - ry mean(s) - yhat ry mean(s yhat)
@@ -686,6 +715,7 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
       }
       IO::store(p, col(k), n, whole(k), live, out);
     }
+    if constexpr (!AHEAD && !BYTES) load_y(row, r + step);
   };
   // every wave takes as many turns as the workgroup's first row needs
   int first = begin + slice * GROUPS;
@@ -726,8 +756,18 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
   };
   keep(e0, 0);
   keep(e1, 1);
-  keep(b0, 2);
-  keep(b1, 3);
+  if constexpr (PART) {
+#pragma unroll
+    for (int what = 0; what < 2; ++what)
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+          if (col(k) + e < n) mine[(2 + what) * (int64_t)n + col(k) + e] = kept[what][(VEC * k + e) / 4][threadIdx.x][e % 4];
+  } else {
+    keep(b0, 2);
+    keep(b1, 3);
+  }
 }
 
 }  // namespace trt

@@ -10,35 +10,36 @@ constexpr int64_t block_chunks(int64_t cols, int dt) {
   return dt == DT_F32 ? (cols + 3) / 4 : (cols + 7) / 8;
 }
 
-// W waves to a row, K 16-byte chunks to a lane, as few waves as hold the row.  f
-// is called with <W, K>.
-template <int K, class F>
-auto with_row_waves(int64_t chunks, F&& f) {
-  const int64_t waves = (chunks + 64 * K - 1) / (64 * K);
-  if (waves <= 1) return f.template operator()<1, K>();
-  if (waves <= 2) return f.template operator()<2, K>();
-  if (waves <= 4) return f.template operator()<4, K>();
-  if (waves <= 6) return f.template operator()<6, K>();
-  if (waves <= 8) return f.template operator()<8, K>();
-  if (waves <= 12) return f.template operator()<12, K>();
-  return f.template operator()<16, K>();
-}
-
+// The shape of a row of `chunks` 16-byte chunks: W waves, K chunks to a lane.  f is
+// called with <W, K>.
 // Forward: one chunk, two from 768 on (16384 rows of 1024 chunks 190 us in 8
 // waves of two, 207 in 16 of one; 4000 rows of 625 52 and 36).
 template <class F>
 auto with_forward_shape(int64_t chunks, F&& f) {
-  if (chunks <= 768) return with_row_waves<1>(chunks, f);
+  if (chunks <= 64) return f.template operator()<1, 1>();
+  if (chunks <= 128) return f.template operator()<2, 1>();
+  if (chunks <= 256) return f.template operator()<4, 1>();
+  if (chunks <= 384) return f.template operator()<6, 1>();
+  if (chunks <= 512) return f.template operator()<8, 1>();
+  if (chunks <= 640) return f.template operator()<10, 1>();
+  if (chunks <= 768) return f.template operator()<12, 1>();
   if (chunks <= 1024) return f.template operator()<8, 2>();
   if (chunks <= 1536) return f.template operator()<12, 2>();
   return f.template operator()<16, 2>();
 }
 
 // Backward: two chunks, so that the vectors and sums that a lane keeps fit beside
-// the rows.
+// the rows; one where three waves to a SIMD then share the work evenly.
 template <class F>
 auto with_block_shape(int64_t chunks, F&& f) {
-  return chunks <= 64 ? f.template operator()<1, 1>() : with_row_waves<2>(chunks, f);
+  if (chunks <= 64) return f.template operator()<1, 1>();
+  if (chunks <= 128) return f.template operator()<1, 2>();
+  if (chunks <= 256) return f.template operator()<2, 2>();
+  if (chunks <= 512) return f.template operator()<4, 2>();
+  if (chunks <= 768) return f.template operator()<12, 1>();
+  if (chunks <= 1024) return f.template operator()<8, 2>();
+  if (chunks <= 1536) return f.template operator()<12, 2>();
+  return f.template operator()<16, 2>();
 }
 
 // Workgroups for `need` turns, at most `most`, each with the same number of
@@ -60,11 +61,11 @@ inline int64_t cheapest_slices(int64_t need, int64_t groups, int64_t most, int64
   return best;
 }
 
-// Forward workgroups, 16 waves to each of the 256 units (a row's own where it
-// has more).
-template <int W>
+// Forward workgroups, up to 20 waves of one chunk to a lane or 16 to each of the 256
+// units, as their registers allow (a row's own where it has more).
+template <int W, int K>
 int64_t forward_slices(int64_t span, int64_t groups) {
-  constexpr int waves = NormShape<W>::THREADS / 64, each = 16 / waves > 0 ? 16 / waves : 1;
+  constexpr int waves = NormShape<W>::THREADS / 64, each = (K == 1 ? 20 : 16) / waves;
   return cheapest_slices((span + NormShape<W>::GROUPS - 1) / NormShape<W>::GROUPS, groups, 256 * each, 1);
 }
 

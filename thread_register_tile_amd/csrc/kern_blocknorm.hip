@@ -31,7 +31,7 @@ hipError_t launch_block_norm(BlockNormArgs a, int dt, hipStream_t s) {
   const int64_t span = each ? a.rows : a.span, groups = (a.rows + span - 1) / span;
   return with_type(dt, [&]<int DT>() {
     return with_forward_shape(block_chunks(a.cols, DT), [&]<int W, int K>() {
-      a.slices = (int32_t)forward_slices<W>(span, groups);
+      a.slices = (int32_t)forward_slices<W, K>(span, groups);
       const dim3 grid(groups * a.slices), block(NormShape<W>::THREADS);
       auto run = [&]<bool TINY>() {
         if (each) return launch(block_norm_kernel<DT, W, K, true, TINY>, grid, block, 0, s, a);
