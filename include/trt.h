@@ -712,7 +712,7 @@ trt_status trt_act8_weight_grad(int64_t tokens, int64_t outputs, int64_t inputs,
  * NULL (no norm follows); dh or dr_out may be NULL (zero), not both; without dh
  * r_out is not read and may be NULL, and dgamma and dbeta are refused.  In the
  * backward pass r_out and y may both be 8-bit rows of trt_act8_pack (scale not
- * NULL; TRT_ERR_ARG for one of them), read as trt_act8_unpack gives them in dtype.
+ * NULL; TRT_ERR_ARG for one of them), taken as the values that they stand for.
  *
  * gate: [ceil(rows / rows_per_gate), cols] of gate_dtype, row i of the block under
  * gate row i / rows_per_gate: one gate for all rows, one for each sequence, one

@@ -1132,8 +1132,8 @@ def block_norm_bwd(dh, dr_out, r_out, y, gate=None, *, post=True, post_gamma=Non
     (dr, dy, dgate, dpost_gamma, dpost_beta, dgamma, dbeta), by
     trt_block_norm_bwd.  Either of dh and dr_out may be None (zero); r_out is
     the forward pass's result, y its input, both tensors or both the (q, scale) of
-    act8_pack, read as act8_unpack gives them in dh's dtype; r_out may be None
-    without dh.  The other arguments are the forward pass's (the gradients do not
+    act8_pack, taken as the values that they stand for; r_out may be None without
+    dh.  The other arguments are the forward pass's (the gradients do not
     depend on beta).  dgate is None without a gate, dpost_gamma and dpost_beta
     without post, dgamma and dbeta without dh, all five with params=False; they
     have their operand's shape and dtype (the parameters' one dtype, float32

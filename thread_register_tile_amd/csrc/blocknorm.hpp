@@ -19,8 +19,9 @@
 // lives in registers from its load to its store, as in the layer norm
 // (layernorm.hpp, whose row cutting, sums and corrected mean this uses).  The
 // stream is kept in binary32 between the sum and the second norm, so h has one
-// rounding.  Backward, r' and y may be 8-bit rows (act8.hpp): they are restored
-// in registers, 33/32 bytes an element instead of two.
+// rounding.  Backward, r' and y may be 8-bit rows (act8.hpp), 33/32 bytes an
+// element instead of two: the sums are those of the integers, each chunk's times
+// its step.
 //
 // A gate row covers `span` rows.  Its gradient, and post_gamma's and post_beta's,
 // all come of two sums over its rows, E0 of e and E1 of e yhat:
@@ -58,19 +59,20 @@ struct RowIO {
   using Q = Act8Chunk<DT>;
   static constexpr int VEC = C::VEC, E = sizeof(typename C::Elem), BITS = 8 * E;
 
+  // where a chunk is read (an offset without a sign: the loads then add it to a
+  // scalar base by themselves)
+  __device__ static uint32_t at(int i, int n) { return (uint32_t)(i < n - VEC ? i : n - VEC); }
   __device__ static u32x4 load(const char* row, int i, int n) {
     if constexpr (TINY) return i < n ? C::load(row, i, n) : u32x4{0u, 0u, 0u, 0u};
-    const int at = i < n - VEC ? i : n - VEC;
-    return __builtin_nontemporal_load(reinterpret_cast<const typename C::Word4*>(row + at * E));
+    return __builtin_nontemporal_load(reinterpret_cast<const typename C::Word4*>(row + at(i, n) * E));
   }
   __device__ static u32x4 load_shared(const char* row, int i, int n) {
     if constexpr (TINY) return i < n ? C::load_shared(row, i, n) : u32x4{0u, 0u, 0u, 0u};
-    const int at = i < n - VEC ? i : n - VEC;
-    return *reinterpret_cast<const typename C::Word4*>(row + at * E);
+    return *reinterpret_cast<const typename C::Word4*>(row + at(i, n) * E);
   }
   __device__ static u32x2 load8(const int8_t* row, int i, int n) {
     if constexpr (TINY) return i < n ? Q::load(row, i, n) : u32x2{0u, 0u};
-    const int8_t* p = row + (i < n - VEC ? i : n - VEC);
+    const int8_t* p = row + at(i, n);
     if constexpr (VEC == 8) return __builtin_nontemporal_load(reinterpret_cast<const u32x2_at1*>(p));
     else return u32x2{__builtin_nontemporal_load(reinterpret_cast<const u32_at1*>(p)), 0u};
   }
@@ -394,6 +396,13 @@ __global__ __launch_bounds__(NormShape<W>::THREADS) void block_norm_kernel(Block
   }
 }
 
+// keep_packed for saved rows of either form.
+template <class V, int K>
+__device__ __forceinline__ void keep_saved(V (&v)[K]) {
+#pragma unroll
+  for (int k = 0; k < K; ++k) asm volatile("" : "+v"(v[k]));
+}
+
 // The backward pass over the rows: workgroup `slice` of a gate row's `slices`
 // takes that row's rows in turn, GROUPS at a time.  Three rounds of sums: the
 // means of r' and y; the spreads, mean(t), mean(t rhat); mean(s), mean(s yhat).
@@ -471,18 +480,23 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
     load_x(q, row);
     load_y(q, row);
   };
-  auto open_saved = [&](u32x4 (&to)[K], const Saved (&v)[K], const uint32_t (&b)[K]) __attribute__((always_inline)) {
+  // An element of a saved row is raw() times the chunk's step: the integer of an
+  // 8-bit row, of which a sum takes the step out, or the element itself and 1.
+  auto open_saved = [&](Saved (&v)[K], float (&step)[K], const uint32_t (&b)[K]) __attribute__((always_inline)) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       if constexpr (BYTES) {
-        u32x2 q = v[k];
-        if (!whole(k)) q = IO::fix8(q, col(k), n);
-        to[k] = Q::restore(q, Q::step(b[k]));
+        step[k] = Q::step(b[k]);
+        if (!whole(k)) v[k] = IO::fix8(v[k], col(k), n);
       } else {
-        to[k] = v[k];
-        if (!whole(k)) to[k] = IO::fix(to[k], col(k), n);
+        step[k] = 1.f;
+        if (!whole(k)) v[k] = IO::fix(v[k], col(k), n);
       }
     }
+  };
+  auto raw = [](const Saved& v, int e) __attribute__((always_inline)) {
+    if constexpr (BYTES) return (float)(int8_t)(v[e / 4] >> (8 * (e & 3)));
+    else return C::elem(v, e);
   };
 
   // gamma and gate post_gamma, zero past the columns: what they multiply adds
@@ -531,12 +545,16 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
   auto body = [&](Row& row, Row& next) __attribute__((always_inline)) {
     const bool live = GROUPS == 1 || r < end;
     if constexpr (AHEAD) load_row(next, r + step);
-    u32x4 (&dh)[K] = row.dh, (&dr)[K] = row.dr, x[K], y[K];
+    u32x4 (&dh)[K] = row.dh, (&dr)[K] = row.dr;
+    Saved x[K], y[K];
+    float xstep[K], ystep[K];
 #pragma unroll
-    for (int k = 0; k < K; ++k)
+    for (int k = 0; k < K; ++k) {
       if (!whole(k)) dh[k] = IO::fix(dh[k], col(k), n), dr[k] = IO::fix(dr[k], col(k), n);
-    open_saved(x, row.x, row.xb);
-    open_saved(y, row.y, row.yb);
+      x[k] = row.x[k], y[k] = row.y[k];
+    }
+    open_saved(x, xstep, row.xb);
+    open_saved(y, ystep, row.yb);
     if constexpr (!AHEAD && BYTES) {
       load_x(row, r + step);
       load_y(row, r + step);
@@ -546,7 +564,11 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
       for (int k = 0; k < K; ++k) dr[k] = none;
     if (!live)
 #pragma unroll
-      for (int k = 0; k < K; ++k) dh[k] = dr[k] = x[k] = y[k] = none;
+      for (int k = 0; k < K; ++k) {
+        dh[k] = dr[k] = none;
+        x[k] = y[k] = Saved{};
+        xstep[k] = ystep[k] = 0.f;
+      }
     // addresses and column tests made anew for each pass over a long row: kept
     // they would take a third of the registers
     if constexpr (K * VEC > 8) asm volatile("" : "+v"(me));
@@ -554,18 +576,22 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
     if constexpr (!RMS) {
       float s[2] = {0.f, 0.f};
 #pragma unroll
-      for (int k = 0; k < K; ++k)
+      for (int k = 0; k < K; ++k) {
+        float c[2] = {0.f, 0.f};
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-          s[0] += C::elem(x[k], e);
-          s[1] += C::elem(y[k], e);
+          c[0] += raw(x[k], e);
+          c[1] += raw(y[k], e);
         }
+        s[0] += xstep[k] * c[0];
+        s[1] += ystep[k] * c[1];
+      }
       meet<W, 2>(s, buf, turn, wave, W * grp);
       mx = rounded(s[0] * inv);
       my = a.post ? rounded(s[1] * inv) : 0.f;
     }
-    keep_packed(x);
-    keep_packed(y);
+    keep_saved(x);
+    keep_saved(y);
     // d = x - mx, f = y - my: d^2, t d, f^2; with the means d, t, f too
     float q[RMS ? 3 : 6];
 #pragma unroll
@@ -574,29 +600,35 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
     for (int k = 0; k < K; ++k) {
       float gm[VEC];
       if constexpr (!KEPT) get_gamma(k, gm);
-      auto add = [&](int e) __attribute__((always_inline)) {
-        const float d = RMS ? C::elem(x[k], e) : C::elem(x[k], e) - mx;
-        const float f = RMS ? C::elem(y[k], e) : C::elem(y[k], e) - my;
-        const float t = C::elem(dh[k], e) * (KEPT ? g1[KEPT ? k : 0][e] : gm[e]);
-        q[0] += d * d;
-        q[1] += t * d;
-        q[2] += f * f;
-        if constexpr (!RMS) {
+      if constexpr (RMS) {
+        float c[3] = {0.f, 0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float d = raw(x[k], e), f = raw(y[k], e);
+          const float t = C::elem(dh[k], e) * (KEPT ? g1[KEPT ? k : 0][e] : gm[e]);
+          c[0] += d * d;
+          c[1] += t * d;
+          c[2] += f * f;
+        }
+        q[0] += xstep[k] * (xstep[k] * c[0]);
+        q[1] += xstep[k] * c[1];
+        q[2] += ystep[k] * (ystep[k] * c[2]);
+      } else {
+        for_elems<VEC>(n - col(k), [&](int e) __attribute__((always_inline)) {
+          const float d = raw(x[k], e) * xstep[k] - mx, f = raw(y[k], e) * ystep[k] - my;
+          const float t = C::elem(dh[k], e) * (KEPT ? g1[KEPT ? k : 0][e] : gm[e]);
+          q[0] += d * d;
+          q[1] += t * d;
+          q[2] += f * f;
           q[3] += d;
           q[4] += t;
           q[5] += f;
-        }
-      };
-      if constexpr (RMS) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) add(e);
-      } else {
-        for_elems<VEC>(n - col(k), add);
+        });
       }
     }
     meet<W, RMS ? 3 : 6>(q, buf, turn, wave, W * grp);
-    keep_packed(x);
-    keep_packed(y);
+    keep_saved(x);
+    keep_saved(y);
     keep_packed(dh);
     keep_packed(dr);
     // (the mean's correction: see layernorm.hpp)
@@ -625,11 +657,12 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
       }
       float out[VEC];
       f32x4 part[2];
+      const float xr = xstep[k] * rx;
       if (a.dh) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
           const float h = C::elem(dh[k], e), t = h * (KEPT ? g1[KEPT ? k : 0][e] : gm[e]);
-          const float xh = (RMS ? C::elem(x[k], e) : (C::elem(x[k], e) - mx) - bx) * rx;
+          const float xh = RMS ? raw(x[k], e) * xr : ((raw(x[k], e) * xstep[k] - mx) - bx) * rx;
           float v = C::elem(dr[k], e) + rx * t;
           if constexpr (!RMS) v -= c1;
           ev[k][e] = v - xh * c2;
@@ -661,7 +694,7 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
           load_values<DT, TINY>(a.post ? a.post_beta : nullptr, a.wide_params, col(k), n, whole(k), 0.f, pb);
 #pragma unroll
           for (int e = 0; e < VEC; ++e) {
-            const float yh = ((C::elem(y[k], e) - my) - by) * ry;
+            const float yh = ((raw(y[k], e) * ystep[k] - my) - by) * ry;
             out[e] = ev[k][e] * (yh * pg[e] + pb[e]);
           }
           if (a.wide_gate && DT != DT_F32) {
@@ -678,20 +711,22 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
 #pragma unroll
         for (int e = 0; e < VEC; ++e) ev[k][e] *= gate[e];
       }
+      float c = 0.f;
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        const float f = RMS ? C::elem(y[k], e) : C::elem(y[k], e) - my;
+        const float f = RMS ? raw(y[k], e) : raw(y[k], e) * ystep[k] - my;
         const float sv = ev[k][e] * (KEPT ? gp[KEPT ? k : 0][e] : pm[e]);
-        s[0] += sv * f;
+        c += sv * f;
         if constexpr (!RMS) s[1] += sv;
       }
+      s[0] += RMS ? ystep[k] * c : c;
     }
     if constexpr (!AHEAD) {
       load_up(row, r + step);
       if constexpr (!BYTES) load_x(row, r + step);
     }
     if (a.post) meet<W, RMS ? 1 : 2>(s, buf, turn, wave, W * grp);
-    keep_packed(y);
+    keep_saved(y);
     // dy = ry s - ry mean(s) - yhat ry mean(s yhat)
     float s1 = 0.f, s2 = 0.f;
     if (a.post) {
@@ -704,9 +739,10 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
     for (int k = 0; k < K; ++k) {
       float pm[VEC], out[VEC];
       if constexpr (!KEPT) get_post(k, pm);
+      const float yr = ystep[k] * ry;
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        const float yh = (RMS ? C::elem(y[k], e) : (C::elem(y[k], e) - my) - by) * ry, v = ev[k][e];
+        const float yh = RMS ? raw(y[k], e) * yr : ((raw(y[k], e) * ystep[k] - my) - by) * ry, v = ev[k][e];
         float o = ry * (v * (KEPT ? gp[KEPT ? k : 0][e] : pm[e]));
         if constexpr (!RMS) o -= s1;
         out[e] = o - yh * s2;
