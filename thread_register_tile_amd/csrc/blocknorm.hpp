@@ -51,7 +51,7 @@ __device__ __forceinline__ const char* row_of(const void* p, bool wide, int64_t 
 // shifts out what lies before the chunk (all of it, where the chunk lies past the
 // row): zeros take its place.  Stores go through a descriptor of the row, at an
 // offset beyond it where the chunk is not whole; the cut chunk of a row whose
-// length VEC does not divide follows element by element.
+// length VEC does not divide follows in pieces.
 // TINY: rows of fewer than VEC elements, read one by one.
 template <int DT, bool TINY>
 struct RowIO {
@@ -109,13 +109,18 @@ struct RowIO {
     }
     const uint32_t off = (uint32_t)i * E;
     __builtin_amdgcn_raw_buffer_store_b128(v, rs, (int)(off | (i + VEC <= n ? 0u : 0x80000000u)), 0, kNonTemporal);
-    if (whole || n % VEC == 0) return;
-    const bool cut = i < n && i + VEC > n;
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      const int at = (int)((off + e * E) | (cut && i + e < n ? 0u : 0x80000000u));
-      if constexpr (DT == DT_F32) __builtin_amdgcn_raw_buffer_store_b32(v[e], rs, at, 0, 0);
-      else __builtin_amdgcn_raw_buffer_store_b16((short)(v[e / 2] >> (16 * (e & 1))), rs, at, 0, 0);
+    const int left = n % VEC;   // of the cut chunk, in pieces of 4, 2 and 1: three more operations at most
+    if (whole || left == 0) return;
+    const uint32_t to = off | (i < n && i + VEC > n ? 0u : 0x80000000u);
+    if constexpr (DT == DT_F32) {
+      if (left & 2) __builtin_amdgcn_raw_buffer_store_b64(u32x2{v[0], v[1]}, rs, (int)to, 0, 0);
+      if (left & 1) __builtin_amdgcn_raw_buffer_store_b32(left & 2 ? v[2] : v[0], rs, (int)(to + (left & 2) * E), 0, 0);
+    } else {
+      if (left & 4) __builtin_amdgcn_raw_buffer_store_b64(u32x2{v[0], v[1]}, rs, (int)to, 0, 0);
+      const uint32_t second = left & 4 ? v[2] : v[0], third = left & 4 ? v[3] : v[1];
+      if (left & 2) __builtin_amdgcn_raw_buffer_store_b32(second, rs, (int)(to + (left & 4) * E), 0, 0);
+      if (left & 1)
+        __builtin_amdgcn_raw_buffer_store_b16((short)(left & 2 ? third : second), rs, (int)(to + (left & 6) * E), 0, 0);
     }
   }
 };
