@@ -241,6 +241,7 @@ __global__ __launch_bounds__(256) void act8_sum_kernel(Act8SumArgs a) {
     const int64_t m = id / runs, c = 4 * (id - m * runs);
     const float* p = a.part + m * a.part_ld + c;
     f32x4 y = *reinterpret_cast<const f32x4*>(p);
+#pragma unroll 8
     for (int s = 1; s < a.slices; ++s) y += *reinterpret_cast<const f32x4*>(p + s * a.step);
 #pragma unroll
     for (int e = 0; e < 4; ++e)
