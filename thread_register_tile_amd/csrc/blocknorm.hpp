@@ -427,7 +427,7 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
   constexpr int HELD = K * (16 + (PART ? 3 : 5) * VEC);
   constexpr bool AHEAD = HELD + 16 * K <= ROOM, KEPT = AHEAD && HELD + 16 * K + 2 * VEC * K <= ROOM;
   __shared__ float buf[2][128];
-  __shared__ float fold[GROUPS > 1 ? GROUPS : 1][GROUPS > 1 ? LANES * VEC * K : 1];
+  __shared__ float fold[GROUPS > 1 ? GROUPS : 1][4][GROUPS > 1 ? LANES * VEC * K : 1];
   __shared__ f32x4 kept[2][PART ? K * VEC / 4 : 1][PART ? 64 * WAVES : 1];   // a lane's own entries
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wave = w % W, grp = w / W;
@@ -772,28 +772,15 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
   }
   if (!a.part) return;
   float* mine = a.part + (int64_t)blockIdx.x * 4 * n;
+  // of several groups: their sums of a column, added in group order
   auto keep = [&](float (&acc)[K][VEC], int what) {
-    if constexpr (GROUPS > 1) {
-      // the groups' sums of a column, added in group order
-      __syncthreads();
 #pragma unroll
-      for (int k = 0; k < K; ++k)
+    for (int k = 0; k < K; ++k)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) fold[grp][VEC * (me + k * LANES) + e] = acc[k][e];
-      __syncthreads();
-      for (int c = threadIdx.x; c < n; c += 64 * WAVES) {
-        float t = fold[0][c];
-#pragma unroll
-        for (int q = 1; q < GROUPS; ++q) t += fold[q][c];
-        mine[what * (int64_t)n + c] = t;
+      for (int e = 0; e < VEC; ++e) {
+        if constexpr (GROUPS > 1) fold[grp][what][VEC * (me + k * LANES) + e] = acc[k][e];
+        else if (col(k) + e < n) mine[what * (int64_t)n + col(k) + e] = acc[k][e];
       }
-    } else {
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e)
-          if (col(k) + e < n) mine[what * (int64_t)n + col(k) + e] = acc[k][e];
-    }
   };
   keep(e0, 0);
   keep(e1, 1);
@@ -808,6 +795,17 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
   } else {
     keep(b0, 2);
     keep(b1, 3);
+  }
+  if constexpr (GROUPS > 1) {
+    __syncthreads();
+    for (int c = threadIdx.x; c < n; c += 64 * WAVES)
+#pragma unroll
+      for (int what = 0; what < 4; ++what) {
+        float t = fold[0][what][c];
+#pragma unroll
+        for (int q = 1; q < GROUPS; ++q) t += fold[q][what][c];
+        mine[what * (int64_t)n + c] = t;
+      }
   }
 }
 
