@@ -423,12 +423,14 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
   constexpr int VEC = C::VEC, LANES = 64 * W, GROUPS = WAVES / W, E = sizeof(typename C::Elem);
   // of 256, 168 and 128 registers; HELD: the rows, e and the sums
   constexpr int ROOM = WAVES <= 8 ? 216 : WAVES <= 12 ? 118 : 78;
-  constexpr bool PART = WAVES > 8 && K * VEC > 8;    // dgamma's and dbeta's sums wait in LDS
+  // of long rows LDS holds what the registers do not: of 16 waves dgamma's and
+  // dbeta's sums, of 12 gamma and post_gamma
+  constexpr bool LONG = WAVES > 8 && K * VEC > 8, PART = LONG && WAVES > 12, VECTORS = LONG && !PART;
   constexpr int HELD = K * (16 + (PART ? 3 : 5) * VEC);
-  constexpr bool AHEAD = HELD + 16 * K <= ROOM, KEPT = AHEAD && HELD + 16 * K + 2 * VEC * K <= ROOM;
+  constexpr bool AHEAD = !LONG && HELD + 16 * K <= ROOM, KEPT = AHEAD && HELD + 16 * K + 2 * VEC * K <= ROOM;
   __shared__ float buf[2][128];
   __shared__ float fold[GROUPS > 1 ? GROUPS : 1][4][GROUPS > 1 ? LANES * VEC * K : 1];
-  __shared__ f32x4 kept[2][PART ? K * VEC / 4 : 1][PART ? 64 * WAVES : 1];   // a lane's own entries
+  __shared__ f32x4 kept[2][LONG ? K * VEC / 4 : 1][LONG ? 64 * WAVES : 1];   // a lane's own entries
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wave = w % W, grp = w / W;
   int me = 64 * wave + (threadIdx.x & 63);
@@ -525,6 +527,33 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
 #pragma unroll
     for (int e = 0; e < VEC; ++e) v[e] *= g[e];
   };
+  // a vector's part of a chunk, where it is not in registers
+  auto vector = [&](int what, int k, float (&v)[VEC]) __attribute__((always_inline)) {
+    if constexpr (VECTORS) {
+#pragma unroll
+      for (int q = 0; q < VEC / 4; ++q) {
+        const f32x4 x = kept[what][k * (VEC / 4) + q][threadIdx.x];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[4 * q + e] = x[e];
+      }
+    } else if (what == 0) {
+      get_gamma(k, v);
+    } else {
+      get_post(k, v);
+    }
+  };
+  if constexpr (VECTORS)
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      float v[2][VEC];
+      get_gamma(k, v[0]);
+      get_post(k, v[1]);
+#pragma unroll
+      for (int q = 0; q < VEC / 4; ++q)
+#pragma unroll
+        for (int what = 0; what < 2; ++what)
+          kept[what][k * (VEC / 4) + q][threadIdx.x] = f32x4{v[what][4 * q], v[what][4 * q + 1], v[what][4 * q + 2], v[what][4 * q + 3]};
+    }
   // two rows' registers, used in turn: the one at work and the one on its way; or
   // one, each part of which is loaded again as soon as it has been used
   Row rows[AHEAD ? 2 : 1];
@@ -604,7 +633,7 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       float gm[VEC];
-      if constexpr (!KEPT) get_gamma(k, gm);
+      if constexpr (!KEPT) vector(0, k, gm);
       if constexpr (RMS) {
         float c[3] = {0.f, 0.f, 0.f};
 #pragma unroll
@@ -657,8 +686,8 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
     for (int k = 0; k < K; ++k) {
       float gm[VEC], pm[VEC];
       if constexpr (!KEPT) {
-        get_gamma(k, gm);
-        get_post(k, pm);
+        vector(0, k, gm);
+        vector(1, k, pm);
       }
       float out[VEC];
       f32x4 part[2];
@@ -743,7 +772,7 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       float pm[VEC], out[VEC];
-      if constexpr (!KEPT) get_post(k, pm);
+      if constexpr (!KEPT) vector(1, k, pm);
       const float yr = ystep[k] * ry;
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
