@@ -423,11 +423,11 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
   constexpr int VEC = C::VEC, LANES = 64 * W, GROUPS = WAVES / W, E = sizeof(typename C::Elem);
   // of 256, 168 and 128 registers; HELD: the rows, e and the sums
   constexpr int ROOM = WAVES <= 8 ? 216 : WAVES <= 12 ? 118 : 78;
-  // of long rows LDS holds what the registers do not: of 16 waves dgamma's and
-  // dbeta's sums, of 12 gamma and post_gamma
-  constexpr bool LONG = WAVES > 8 && K * VEC > 8, PART = LONG && WAVES > 12, VECTORS = LONG && !PART;
+  // of long rows LDS holds what the registers do not: gamma and post_gamma, or of
+  // 16 waves of 16-bit rows dgamma's and dbeta's sums
+  constexpr bool LONG = WAVES > 8 && K > 1, PART = LONG && WAVES > 12 && VEC == 8, VECTORS = LONG && !PART;
   constexpr int HELD = K * (16 + (PART ? 3 : 5) * VEC);
-  constexpr bool AHEAD = !LONG && HELD + 16 * K <= ROOM, KEPT = AHEAD && HELD + 16 * K + 2 * VEC * K <= ROOM;
+  constexpr bool AHEAD = !(LONG && VEC == 8) && HELD + 16 * K <= ROOM, KEPT = AHEAD && !VECTORS && HELD + 16 * K + 2 * VEC * K <= ROOM;
   __shared__ float buf[2][128];
   __shared__ float fold[GROUPS > 1 ? GROUPS : 1][4][GROUPS > 1 ? LANES * VEC * K : 1];
   __shared__ f32x4 kept[2][LONG ? K * VEC / 4 : 1][LONG ? 64 * WAVES : 1];   // a lane's own entries
