@@ -250,7 +250,8 @@ __device__ __forceinline__ void meet(float (&v)[N], float (*buf)[128], int& turn
 
 // EACH: gate rows of few rows, loaded with each of them; otherwise a workgroup's
 // rows lie in one gate row, and gate and post norm's parameters are one product.
-// KEEP: the vectors stay in registers (of 16 waves to a row none are left).
+// KEEP: the vectors stay in registers; of 16 waves to a row none are left, and LDS
+// holds the factors, the summands (where there are any) are read with each row.
 template <int DT, int W, int K, bool EACH, bool TINY>
 __global__ __launch_bounds__(NormShape<W>::THREADS) void block_norm_kernel(BlockNormArgs a) {
   using C = RowChunk<DT>;
@@ -277,19 +278,34 @@ __global__ __launch_bounds__(NormShape<W>::THREADS) void block_norm_kernel(Block
 
   // u1 yhat + u0 is what the gate multiplies (EACH) or what joins the stream
   float u1[KEEP ? K : 1][VEC], u0[KEEP ? K : 1][VEC], gamma[KEEP ? K : 1][VEC], beta[KEEP ? K : 1][VEC];
-  auto post = [&](int k, int to) {
-    load_values<DT, TINY>(a.post ? a.post_gamma : nullptr, a.wide_params, col(k), n, whole(k), 1.f, u1[to]);
-    load_values<DT, TINY>(a.post ? a.post_beta : nullptr, a.wide_params, col(k), n, whole(k), 0.f, u0[to]);
-    if (!EACH && a.gate) {
-      float g[VEC];
-      load_values<DT, TINY>(row_of(a.gate, a.wide_gate, gate_row, a.ldg, E), a.wide_gate, col(k), n, whole(k), 1.f, g);
+  __shared__ f32x4 kept[2][KEEP ? 1 : K * VEC / 4][KEEP ? 1 : LANES];   // a lane's own entries
+  auto gated = [&](int k, float (&v)[VEC]) __attribute__((always_inline)) {
+    if (EACH || !a.gate) return;
+    float g[VEC];
+    load_values<DT, TINY>(row_of(a.gate, a.wide_gate, gate_row, a.ldg, E), a.wide_gate, col(k), n, whole(k), 1.f, g);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) u1[to][e] *= g[e], u0[to][e] *= g[e];
-    }
+    for (int e = 0; e < VEC; ++e) v[e] *= g[e];
   };
-  auto pre = [&](int k, int to) {
-    load_values<DT, TINY>(a.gamma, a.wide_params, col(k), n, whole(k), 1.f, gamma[to]);
-    load_values<DT, TINY>(a.beta, a.wide_params, col(k), n, whole(k), 0.f, beta[to]);
+  auto factors = [&](int k, float (&u)[VEC], float (&g)[VEC]) __attribute__((always_inline)) {
+    load_values<DT, TINY>(a.post ? a.post_gamma : nullptr, a.wide_params, col(k), n, whole(k), 1.f, u);
+    load_values<DT, TINY>(a.gamma, a.wide_params, col(k), n, whole(k), 1.f, g);
+    gated(k, u);
+  };
+  const void* const post_beta = a.post ? a.post_beta : nullptr;
+  auto post_summand = [&](int k, float (&v)[VEC]) __attribute__((always_inline)) {
+    load_values<DT, TINY>(post_beta, a.wide_params, col(k), n, whole(k), 0.f, v);
+    if (post_beta) gated(k, v);
+  };
+  auto summand = [&](int k, float (&v)[VEC]) __attribute__((always_inline)) {
+    load_values<DT, TINY>(a.beta, a.wide_params, col(k), n, whole(k), 0.f, v);
+  };
+  auto factor_of = [&](int what, int k, float (&v)[VEC]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int q = 0; q < VEC / 4; ++q) {
+      const f32x4 x = kept[what][k * (VEC / 4) + q][KEEP ? 0 : threadIdx.x];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[4 * q + e] = x[e];
+    }
   };
 
   // two rows' registers, used in turn: the one at work and the one on its way
@@ -309,7 +325,22 @@ __global__ __launch_bounds__(NormShape<W>::THREADS) void block_norm_kernel(Block
   load_row(rows[0], r);
   if constexpr (KEEP)
 #pragma unroll
-    for (int k = 0; k < K; ++k) pre(k, k), post(k, k);
+    for (int k = 0; k < K; ++k) {
+      factors(k, u1[k], gamma[k]);
+      post_summand(k, u0[k]);
+      summand(k, beta[k]);
+    }
+  else
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      float v[2][VEC];
+      factors(k, v[0], v[1]);
+#pragma unroll
+      for (int q = 0; q < VEC / 4; ++q)
+#pragma unroll
+        for (int what = 0; what < 2; ++what)
+          kept[what][k * (VEC / 4) + q][threadIdx.x] = f32x4{v[what][4 * q], v[what][4 * q + 1], v[what][4 * q + 2], v[what][4 * q + 3]};
+    }
   auto body = [&](Row& row, Row& next) __attribute__((always_inline)) {
     auto &x = row.x, &y = row.y;
     float g[EACH ? K : 1][VEC];
@@ -354,7 +385,10 @@ __global__ __launch_bounds__(NormShape<W>::THREADS) void block_norm_kernel(Block
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int to = KEEP ? k : 0;
-      if constexpr (!KEEP) post(k, 0);
+      if constexpr (!KEEP) {
+        factor_of(0, k, u1[0]);
+        post_summand(k, u0[0]);
+      }
 #pragma unroll
       for (int e = 0; e < VEC; ++e) z[k][e] = 0.f;
       for_elems<VEC>(n - col(k), [&](int e) {
@@ -386,7 +420,10 @@ __global__ __launch_bounds__(NormShape<W>::THREADS) void block_norm_kernel(Block
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int to = KEEP ? k : 0;
-      if constexpr (!KEEP) pre(k, 0);
+      if constexpr (!KEEP) {
+        factor_of(1, k, gamma[0]);
+        summand(k, beta[0]);
+      }
       float h[VEC];
 #pragma unroll
       for (int e = 0; e < VEC; ++e) h[e] = ((z[k][e] - m) - dbar) * rstd * gamma[to][e] + beta[to][e];
