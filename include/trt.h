@@ -641,9 +641,9 @@ trt_status trt_linear_xent_bwd(int64_t tokens, int64_t vocab, int64_t width,
  *   trt_act8_weight_grad:  dw = dy^T . x, x as trt_act8_unpack gives it in
  *                     in_dtype, the sum over the tokens.
  *
- * An element is off by at most 2^-7 of the largest power of two in its block's
- * largest magnitude (half that where it does not round up to 128 steps), or by
- * 2^-127 where that is more.  Unpacking is exact in bf16 and binary32 for what
+ * An element is off by at most half a step, 2^-7 of the largest power of two in
+ * its block's largest magnitude (2^-127 where that is more), or a whole one where
+ * it would round up to 128 steps.  Unpacking is exact in bf16 and binary32 for what
  * trt_act8_pack made, and in binary16 where x was binary16.
  *
  * x: rows x cols of dtype (TRT_F16, TRT_BF16 or TRT_F32); q: rows x cols bytes;

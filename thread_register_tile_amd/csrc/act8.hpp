@@ -12,8 +12,8 @@
 // and binary16 where x was binary16.  A block that holds an infinity or NaN has
 // X = 255 and stands for NaN throughout: what was not finite does not come back
 // as a number.  Integers rather than 8-bit floats: at the same 8.25 bits an
-// element they leave a normal distribution's rows off by 0.5 % where 3 bits of
-// mantissa leave 2.6 %.
+// element they leave a normal distribution's rows off by 0.8 % of their norm where 3 bits
+// of mantissa leave 2.7 %.
 //
 // What bounds it: memory, x once and 33/32 bytes an element.  A thread takes
 // four chunks of 16 bytes of x, 256 chunks apart, all loaded before the first

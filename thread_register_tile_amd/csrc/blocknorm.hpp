@@ -46,7 +46,7 @@ __device__ __forceinline__ const char* row_of(const void* p, bool wide, int64_t 
 // A row's chunks without a branch: with memory operations under a condition the
 // compiler counts the fewest that may be in flight, and a wait for the row at
 // work then waits for the next one's loads or the last one's stores too (16384 x
-// 8192 bf16 backward from 8-bit rows 400 us, 280 without).  A row of n >= VEC
+// 8192 bf16 backward from 8-bit rows 398 us, 266 without).  A row of n >= VEC
 // elements is read VEC at a time from no further than its last VEC, and `fix`
 // shifts out what lies before the chunk (all of it, where the chunk lies past the
 // row): zeros take its place.  Stores go through a descriptor of the row, at an
@@ -448,8 +448,9 @@ __device__ __forceinline__ void keep_saved(V (&v)[K]) {
 // The backward pass over the rows: workgroup `slice` of a gate row's `slices`
 // takes that row's rows in turn, GROUPS at a time.  Three rounds of sums: the
 // means of r' and y; the spreads, mean(t), mean(t rhat); mean(s), mean(s yhat).
-// RMS: without the means, two rounds of four and one (a third of the arithmetic,
-// which with 8-bit rows takes as long as the memory).
+// RMS: without the means, two rounds, of three sums and one (16384 x 8192 bf16 from
+// 8-bit rows 255 to 265 us against 320: the arithmetic, 50 instructions an element
+// and a third more with the means, takes as long as the memory).
 // AHEAD: the next row is loaded ahead, KEPT: gamma and post_gamma stay in
 // registers, where the sums leave room for them.
 template <int DT, bool BYTES, int W, int K, int WAVES, bool RMS, bool TINY>
