@@ -13,6 +13,11 @@ call raises -- there is no fallback path.
     dx, dgamma, dbeta = trt.layernorm_bwd(dy, x, gamma)
     loss, lse = trt.linear_xent(x, W, target)   # cross entropy of x @ W.T
     dx, dW = trt.linear_xent_bwd(x, W, target, lse, dloss)
+    r, h = trt.block_norm(r0, y, gate)          # r = r0 + gate N(y), h = N(r)
+    grads = trt.block_norm_bwd(dh, dr, r, y, gate)
+    q, scale = trt.act8_pack(x)                 # x in 8 bits, a scale to 32 columns
+    x = trt.act8_unpack(q, scale, torch.bfloat16)
+    dW = trt.act8_weight_grad(dy, q, scale)     # dy.T @ x
 """
 import ctypes
 import os

@@ -12,8 +12,9 @@ constexpr int64_t block_chunks(int64_t cols, int dt) {
 
 // The shape of a row of `chunks` 16-byte chunks: W waves, K chunks to a lane.  f is
 // called with <W, K>.
-// Forward: one chunk, two from 768 on (16384 rows of 1024 chunks 190 us in 8
-// waves of two, 207 in 16 of one; 4000 rows of 625 52 and 36).
+// Forward: one chunk up to 768 chunks, two beyond (4000 rows of 625 chunks take 36 us
+// in 10 waves of one, 52 in 8 of two; 16384 rows of 1024 190 in 8 of two, 207 in 16
+// of one).
 template <class F>
 auto with_forward_shape(int64_t chunks, F&& f) {
   if (chunks <= 64) return f.template operator()<1, 1>();
