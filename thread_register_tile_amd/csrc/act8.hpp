@@ -191,9 +191,9 @@ __device__ __forceinline__ void act8_restore(const Act8Args& a, int64_t ldo, int
     if (row[j] >= a.rows || col[j] >= n) continue;
     char* p = static_cast<char*>(a.out) + row[j] * ldo * (int64_t)sizeof(typename C::Elem);
     const float s = Q::step(byte[j]);
-    if constexpr (WHOLE) {
-      u32x4 v = Q::restore(q[j], s);
-      *reinterpret_cast<u32x4*>(p + col[j] * (int)sizeof(typename C::Elem)) = v;
+    if (WHOLE || col[j] + VEC <= n) {
+      using Word4 = std::conditional_t<WHOLE, u32x4, typename C::Word4>;
+      *reinterpret_cast<Word4*>(p + col[j] * (int)sizeof(typename C::Elem)) = Q::restore(q[j], s);
     } else {
       float y[VEC];
 #pragma unroll
