@@ -159,3 +159,19 @@ def test_gradients_against_differences():
                 fd = ((loss(up) - loss(down)) / (2 * step_)).item()
                 an = (g.double() * d).sum().item()
                 assert abs(fd - an) <= 1e-2 * max(abs(an), g.norm().item() / g.numel() ** 0.5), (name, rms, post, fd, an)
+
+
+@pytest.mark.parametrize("cols", [5, 520, 1500, 2056, 8200, 16384])
+@pytest.mark.parametrize("rms", [False, True])
+@pytest.mark.parametrize("bits", [8, 16])
+def test_output_that_is_not_finite_without_its_norm(cols, rms, bits):
+    """Without the post norm dy = gate dr_out (h without a gradient) whatever y
+    holds: products of two bf16 values, exact in binary32 and rounded once."""
+    gen = torch.Generator(device="cuda").manual_seed(cols)
+    y, dr = (torch.randn(70, cols, device="cuda", generator=gen).to(BF16) for _ in range(2))
+    gate = torch.randn(cols, device="cuda", generator=gen).to(BF16)
+    y[3, cols // 2], y[4, 0], y[5, -1] = float("inf"), float("nan"), float("-inf")
+    saved = trt.act8_pack(y) if bits == 8 else y
+    got = trt.block_norm_bwd(None, dr, None, saved, gate, post=False, rms=rms, params=False)
+    assert torch.equal(got[0], dr)
+    assert torch.equal(got[1], (gate.float() * dr.float()).to(BF16))

@@ -549,6 +549,14 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
     else return C::elem(v, e);
   };
 
+  // of 8-bit rows a chunk's sum of u v, an exact integer
+  auto dot = [](const Saved& u, const Saved& v) __attribute__((always_inline)) {
+    int c = 0;
+#pragma unroll
+    for (int w = 0; w < VEC / 4; ++w) c = __builtin_amdgcn_sdot4((int)u[w], (int)v[w], c, false);
+    return (float)c;
+  };
+
   // gamma and gate post_gamma, zero past the columns: what they multiply adds
   // nothing to a sum there
   float g1[KEPT ? K : 1][VEC], gp[KEPT ? K : 1][VEC];
@@ -650,18 +658,27 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
     // they would take a third of the registers
     if constexpr (K * VEC > 8) asm volatile("" : "+v"(me));
     float mx = 0.f, my = 0.f;
+    float xsum[K], ysum[K];   // BYTES: each chunk's
     if constexpr (!RMS) {
       float s[2] = {0.f, 0.f};
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         float c[2] = {0.f, 0.f};
+        if constexpr (BYTES) {
+          const Saved ones = {0x01010101u, 0x01010101u};
+          c[0] = dot(x[k], ones);
+          c[1] = dot(y[k], ones);
+        } else {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          c[0] += raw(x[k], e);
-          c[1] += raw(y[k], e);
+          for (int e = 0; e < VEC; ++e) {
+            c[0] += raw(x[k], e);
+            c[1] += raw(y[k], e);
+          }
         }
-        s[0] += xstep[k] * c[0];
-        s[1] += ystep[k] * c[1];
+        xsum[k] = xstep[k] * c[0];
+        ysum[k] = ystep[k] * c[1];
+        s[0] += xsum[k];
+        s[1] += ysum[k];
       }
       meet<W, 2>(s, buf, turn, wave, W * grp);
       mx = rounded(s[0] * inv);
@@ -679,13 +696,14 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
       if constexpr (!KEPT) vector(0, k, gm);
       if constexpr (RMS) {
         float c[3] = {0.f, 0.f, 0.f};
+        if constexpr (BYTES) c[0] = dot(x[k], x[k]), c[2] = dot(y[k], y[k]);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
           const float d = raw(x[k], e), f = raw(y[k], e);
           const float t = C::elem(dh[k], e) * (KEPT ? g1[KEPT ? k : 0][e] : gm[e]);
-          c[0] += d * d;
+          if constexpr (!BYTES) c[0] += d * d;
           c[1] += t * d;
-          c[2] += f * f;
+          if constexpr (!BYTES) c[2] += f * f;
         }
         q[0] += xstep[k] * (xstep[k] * c[0]);
         q[1] += xstep[k] * c[1];
@@ -697,10 +715,16 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
           q[0] += d * d;
           q[1] += t * d;
           q[2] += f * f;
-          q[3] += d;
+          if constexpr (!BYTES) q[3] += d;
           q[4] += t;
-          q[5] += f;
+          if constexpr (!BYTES) q[5] += f;
         });
+        if constexpr (BYTES) {
+          const int left = n - col(k);
+          const float of = (float)(left < 0 ? 0 : left < VEC ? left : VEC);
+          q[3] += xsum[k] - of * mx;
+          q[5] += ysum[k] - of * my;
+        }
       }
     }
     meet<W, RMS ? 3 : 6>(q, buf, turn, wave, W * grp);
@@ -717,8 +741,8 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
     }
     const float rx = live ? block_rstd(q[0] * inv - bx * bx, a.eps) : 0.f;
     const float ry = !live ? 0.f : a.post ? block_rstd(q[2] * inv - by * by, a.eps) : 1.f;
-    // e = dr + rx t - rx mean(t) - rhat rx mean(t rhat)
-    const float c1 = rx * tbar, c2 = rx * (rx * (q[1] * inv - bx * tbar));
+    // e = dr + rx (t - mean(t)) - rhat rx mean(t rhat), rhat = d rx - bx rx
+    const float c2 = rx * (rx * (q[1] * inv - bx * tbar)), xo = -bx * rx, yo = -by * ry;
     if constexpr (K * VEC > 8) asm volatile("" : "+v"(me));
     float ev[K][VEC];
     float s[RMS ? 1 : 2];
@@ -738,11 +762,11 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
       if (a.dh) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-          const float h = C::elem(dh[k], e), t = h * (KEPT ? g1[KEPT ? k : 0][e] : gm[e]);
-          const float xh = RMS ? raw(x[k], e) * xr : ((raw(x[k], e) * xstep[k] - mx) - bx) * rx;
-          float v = C::elem(dr[k], e) + rx * t;
-          if constexpr (!RMS) v -= c1;
-          ev[k][e] = v - xh * c2;
+          const float h = C::elem(dh[k], e);
+          float t = h * (KEPT ? g1[KEPT ? k : 0][e] : gm[e]);
+          if constexpr (!RMS) t -= tbar;
+          const float xh = RMS ? raw(x[k], e) * xr : (raw(x[k], e) * xstep[k] - mx) * rx + xo;
+          ev[k][e] = (C::elem(dr[k], e) + rx * t) - xh * c2;
           if constexpr (!PART) {
             b0[k][e] += h;
             b1[k][e] += h * xh;
@@ -771,7 +795,7 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
           load_values<DT, TINY>(a.post ? a.post_beta : nullptr, a.wide_params, col(k), n, whole(k), 0.f, pb);
 #pragma unroll
           for (int e = 0; e < VEC; ++e) {
-            const float yh = ((raw(y[k], e) * ystep[k] - my) - by) * ry;
+            const float yh = (raw(y[k], e) * ystep[k] - my) * ry + yo;
             out[e] = ev[k][e] * (yh * pg[e] + pb[e]);
           }
           if (a.wide_gate && DT != DT_F32) {
@@ -804,11 +828,10 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
     }
     if (a.post) meet<W, RMS ? 1 : 2>(s, buf, turn, wave, W * grp);
     keep_saved(y);
-    // dy = ry s - ry mean(s) - yhat ry mean(s yhat)
-    float s1 = 0.f, s2 = 0.f;
+    // dy = ry (s - mean(s)) - yhat ry mean(s yhat)
+    float sbar = 0.f, s2 = 0.f;
     if (a.post) {
-      const float sbar = RMS ? 0.f : s[RMS ? 0 : 1] * inv;
-      s1 = ry * sbar;
+      if constexpr (!RMS) sbar = s[1] * inv;
       s2 = ry * (ry * (s[0] * inv - by * sbar));
     }
     p = static_cast<char*>(a.out_y) + r * a.ld_y * (int64_t)E;
@@ -817,15 +840,18 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
       float pm[VEC], out[VEC];
       if constexpr (!KEPT) vector(1, k, pm);
       const float yr = ystep[k] * ry;
+      float yh[VEC];
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        const float yh = RMS ? raw(y[k], e) * yr : ((raw(y[k], e) * ystep[k] - my) - by) * ry, v = ev[k][e];
-        float o = ry * (v * (KEPT ? gp[KEPT ? k : 0][e] : pm[e]));
-        if constexpr (!RMS) o -= s1;
-        out[e] = o - yh * s2;
-        e0[k][e] += v;
-        e1[k][e] += v * yh;
+        yh[e] = RMS ? raw(y[k], e) * yr : (raw(y[k], e) * ystep[k] - my) * ry + yo;
+        out[e] = ev[k][e] * (KEPT ? gp[KEPT ? k : 0][e] : pm[e]);
+        e0[k][e] += ev[k][e];
+        e1[k][e] += ev[k][e] * yh[e];
       }
+      // (without the norm y is no part of it, whatever it holds)
+      if (a.post)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) out[e] = ry * (RMS ? out[e] : out[e] - sbar) - yh[e] * s2;
       IO::store(p, col(k), n, whole(k), live, out);
     }
     if constexpr (!AHEAD && !BYTES) load_y(row, r + step);
