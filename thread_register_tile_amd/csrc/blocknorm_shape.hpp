@@ -14,11 +14,12 @@ constexpr int64_t block_chunks(int64_t cols, int dt) {
 // called with <W, K>.
 // Forward: one chunk up to 768 chunks, two beyond (4000 rows of 625 chunks take 36 us
 // in 10 waves of one, 52 in 8 of two; 16384 rows of 1024 190 in 8 of two, 207 in 16
-// of one).
+// of one; 60000 rows of 138 119 in 3 of one, 135 in 4 of one).
 template <class F>
 auto with_forward_shape(int64_t chunks, F&& f) {
   if (chunks <= 64) return f.template operator()<1, 1>();
   if (chunks <= 128) return f.template operator()<2, 1>();
+  if (chunks <= 192) return f.template operator()<3, 1>();
   if (chunks <= 256) return f.template operator()<4, 1>();
   if (chunks <= 384) return f.template operator()<6, 1>();
   if (chunks <= 512) return f.template operator()<8, 1>();
