@@ -73,19 +73,38 @@ constexpr int64_t kAct8MaxTokens = int64_t(1) << 23, kAct8MaxWidth = int64_t(1) 
 // than 2^16 of them.
 constexpr int64_t kAct8MaxInPlace = int64_t(1) << 21;
 
-// Tiles are as the cross entropy's weight gradient has them, K is cut as its
-// input gradient's is where they are few: tokens are long and outputs x inputs
-// small in small models.  Slices also keep each operand's extent below 2 GiB.
+// Time of the product cut into s slices, in picoseconds: what a unit's tiles take for
+// each token (alone 5.5 to 7.5 ns of a 128x128 tile and 14.5 to 22 of a 256x256 one,
+// as fewer or more of the 256 units share the power; in turn 6.8 and 21), what a tile
+// costs beside them, and with slices their results' way to memory and back.
+constexpr int64_t act8_cut_cost(int64_t tokens, int64_t outputs, int64_t inputs, int64_t s, bool wide) {
+  const int64_t tile = wide ? 256 : 128;
+  const int64_t groups = ((outputs + tile - 1) / tile) * ((inputs + tile - 1) / tile) * s, rounds = (groups + 255) / 256;
+  const int64_t each = wide ? (rounds > 1 ? 21000 : 14500 + 7500 * groups / 256)
+                            : (rounds > 1 ? 6800 : 5500 + 2000 * groups / 256);
+  const int64_t joined = s > 1 ? 3'000'000 + s * outputs * inputs * 11 / 10 : 0;
+  return rounds * xent_slice((uint32_t)s, (uint32_t)tokens) * each + 5'000'000 + joined;
+}
+
+// The cheapest of tiles and slices: in small models tokens are long, and outputs x
+// inputs have few tiles.  At least 512 tokens to a slice, and 256-wide tiles from 769
+// tokens on (few are all store, and two workgroups to a unit store faster).  Measured
+// with one slice of 128-wide tiles, with two, and with 256-wide tiles in as many as
+// suit them: 2048 tokens x 2048 x 2048 30, 41, 46 us, 8192 x 3000 x 1500 126, 123, 96, 16384 x
+// 2048 x 2048 142, 150, 138.  Slices also keep each operand's extent below 2 GiB.
 constexpr Act8WeightPlan act8_weight_plan(int64_t tokens, int64_t outputs, int64_t inputs,
                                           int64_t lddy, bool in_place) {
   Act8WeightPlan p{};
-  p.wide = tokens > 768 && xent_wide(outputs, inputs);
   p.x_ld = round_up(inputs, 8);
   p.dy_ld = in_place ? 0 : round_up(outputs, 8);
   const int64_t dy_ld = in_place ? lddy : p.dy_ld, ld = dy_ld > p.x_ld ? dy_ld : p.x_ld;
   const int64_t most = kAct8Extent / (2 * ld) / 64 * 64;   // tokens below 2 GiB
-  p.slices = xent_slices(outputs, inputs, tokens, p.wide);
-  if (p.slices * most < tokens) p.slices = (tokens + most - 1) / most;
+  const int64_t least = (tokens + most - 1) / most;
+  int64_t cost = -1;
+  for (int64_t s = least; s == least || (s <= kXentMostSlices && s * 512 <= tokens); ++s)
+    for (int wide = tokens > 768; wide >= 0; --wide)
+      if (const int64_t c = act8_cut_cost(tokens, outputs, inputs, s, wide); cost < 0 || c < cost)
+        cost = c, p.slices = s, p.wide = wide;
   p.slice = xent_slice((uint32_t)p.slices, (uint32_t)tokens);
   p.slices = (tokens + p.slice - 1) / p.slice;
   p.part_ld = round_up(inputs, 4);
