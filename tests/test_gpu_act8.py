@@ -245,3 +245,19 @@ def test_graph_and_streams():
         torch.cuda.synchronize()
         assert torch.equal(back, b) and torch.equal(dw, eager)
         assert (f64(dw) == f64(a).T @ f64(b)).all()
+
+
+@pytest.mark.parametrize("odt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("tokens,outputs,inputs", [(8200, 2999, 1501), (8192, 3000, 1500), (6000, 1000, 1000), (16384, 512, 520),
+                                                   (2048, 2048, 2048), (1700, 3000, 3000)])
+def test_weight_grad_of_slices_and_tiles(tokens, outputs, inputs, odt):
+    """Either size of tile, in one slice and in several: integers whose every
+    partial sum is below 2^24, so that torch's binary32 product is exact too."""
+    gen = torch.Generator(device="cuda").manual_seed(tokens)
+    dy = torch.randint(-2, 3, (tokens, outputs), device="cuda", generator=gen).to(torch.bfloat16)
+    x = torch.randint(-3, 4, (tokens, inputs), device="cuda", generator=gen).to(torch.bfloat16)
+    need = trt.act8_weight_grad_workspace_size(tokens, outputs, inputs, dy.data_ptr())
+    ws = torch.full((need + 64,), 0xFF, dtype=torch.uint8, device="cuda")
+    got = trt.act8_weight_grad(dy, *trt.act8_pack(x), out_dtype=odt, workspace=ws[:need])
+    assert torch.equal(got, torch.mm(dy.float().t().contiguous(), x.float()).to(odt))
+    assert (ws[need:] == 0xFF).all()
