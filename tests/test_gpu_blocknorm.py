@@ -277,6 +277,12 @@ def test_rows_far_from_zero(mean, scale):
     run_case(40, 4100, BF16, mean=mean, scale=scale, rms=True)
 
 
+@pytest.mark.parametrize("mean,scale", [(100.0, 1.0), (0.0, 1e-3), (0.0, 1e4)])
+def test_rows_far_from_zero_in_8_bits(mean, scale):
+    for cols, dtype in ((1111, F32), (4100, BF16), (16384, BF16)):
+        run_case(20, cols, dtype, mean=mean, scale=scale, saved="8bit")
+
+
 def test_leading_dimensions_and_broadcast_gates():
     x, y = (torch.randn(3, 5, 40, dtype=BF16, device="cuda") for _ in range(2))
     for gate, rows in ((torch.randn(3, 1, 40, device="cuda"), 5), (torch.randn(1, 1, 40, device="cuda"), 15),
