@@ -261,3 +261,16 @@ def test_weight_grad_of_slices_and_tiles(tokens, outputs, inputs, odt):
     got = trt.act8_weight_grad(dy, *trt.act8_pack(x), out_dtype=odt, workspace=ws[:need])
     assert torch.equal(got, torch.mm(dy.float().t().contiguous(), x.float()).to(odt))
     assert (ws[need:] == 0xFF).all()
+
+
+@pytest.mark.parametrize("tokens,outputs,inputs", [(2_097_252, 72, 1100), (2_097_252, 1101, 40), (66_000, 128, 16400), (140_000, 8200, 300)])
+def test_weight_grad_of_operands_past_2_gib(tokens, outputs, inputs):
+    """x or dy of 2 to 4.6 GB, taken in slices: exact as above."""
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    dy = torch.randint(-1, 2, (tokens, outputs), device="cuda", generator=gen).to(torch.bfloat16)
+    x = torch.randint(-3, 4, (tokens, inputs), device="cuda", generator=gen).to(torch.bfloat16)
+    got = trt.act8_weight_grad(dy, *trt.act8_pack(x), out_dtype=torch.float32)
+    want = torch.zeros(outputs, inputs, device="cuda")
+    for at in range(0, tokens, 30_000):
+        want += torch.mm(dy[at:at + 30_000].float().t().contiguous(), x[at:at + 30_000].float())
+    assert torch.equal(got, want)

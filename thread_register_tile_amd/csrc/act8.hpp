@@ -19,8 +19,8 @@
 // four chunks of 16 bytes of x, 256 chunks apart, all loaded before the first
 // is used; a block's four (binary32: eight) chunks sit in neighbouring lanes,
 // whose maximum takes two (three) data-parallel moves.  Measured: 16384 x 8192 bf16
-// packed in 67 us (6.0 TB/s), restored in 71 to 73 (5.6); 4001 x 1023 binary32, whose
-// rows are not aligned, in 7.2 and 10.2.
+// packed in 67 to 69 us (6.0 TB/s), restored in 67 (6.1); 4001 x 1023 binary32, whose
+// rows are not aligned, in 6.5 and 8.5, among other work 7 and 11.
 #pragma once
 
 #include "act8_args.hpp"

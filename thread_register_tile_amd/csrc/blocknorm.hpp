@@ -451,13 +451,13 @@ __device__ __forceinline__ void keep_saved(V (&v)[K]) {
 // takes that row's rows in turn, GROUPS at a time.  Three rounds of sums: the
 // means of r' and y; the spreads, mean(t), mean(t rhat); mean(s), mean(s yhat).
 // RMS: without the means, two rounds, of three sums and one (16384 x 8192 bf16 from
-// 8-bit rows 255 to 265 us against 320: the arithmetic, 50 instructions an element
-// and a third more with the means, takes as long as the memory).
+// 8-bit rows 250 to 265 us against 310: the arithmetic, 40 instructions an element
+// and a fifth more with the means, takes over half the memory's time).
 // AHEAD: the next row is loaded ahead, KEPT: gamma and post_gamma stay in
 // registers, where the sums leave room for them.
 // Measured (this kernel alone): 16384 x 8192 bf16 from 8-bit rows 250 us (5.1 TB/s, the
-// vector units issuing 55 % of the time), 4001 x 1023 binary32 23.5 (four turns of
-// rows that are not aligned), 128 x 1024 f16 6.9.
+// vector units issuing 54 % of the time), 4001 x 1023 binary32 23.7 (four turns of
+// rows that are not aligned), 128 x 1024 f16 7.2.
 template <int DT, bool BYTES, int W, int K, int WAVES, bool RMS, bool TINY>
 __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArgs a) {
   using C = RowChunk<DT>;
