@@ -56,13 +56,18 @@ constexpr int64_t even_grid(int64_t need, int64_t most) {
 }
 
 // Slices of a gate row of `need` turns, where `most` workgroups run at a time: the
-// number that takes the least turns, counting a round's start and end as `beside`.
-inline int64_t cheapest_slices(int64_t need, int64_t groups, int64_t most, int64_t beside) {
+// number that takes the least turns, counting a round's start and end as `beside`,
+// of up to four rounds.  For each number of rounds that is the most slices that fit,
+// or the fewest with as many turns.
+constexpr int64_t cheapest_slices(int64_t need, int64_t groups, int64_t most, int64_t beside) {
   if (groups == 1) return even_grid(need, most);
-  int64_t best = 1, least = -1;
-  for (int64_t s = 1; s <= need && (s == 1 || s * groups <= 4 * most); ++s) {
+  int64_t best = 1, least = (groups + most - 1) / most * (need + beside);
+  for (int64_t rounds = 1; rounds <= 4; ++rounds) {
+    int64_t s = rounds * most / groups;
+    if (s < 1) continue;
+    s = even_grid(need, s < need ? s : need);
     const int64_t cost = (s * groups + most - 1) / most * ((need + s - 1) / s + beside);
-    if (least < 0 || cost < least) best = s, least = cost;
+    if (cost < least) best = s, least = cost;
   }
   return best;
 }
