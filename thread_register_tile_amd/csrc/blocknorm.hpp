@@ -250,9 +250,9 @@ __device__ __forceinline__ void meet(float (&v)[N], float (*buf)[128], int& turn
 
 // The gate row of a workgroup and its slice of that row's rows.  Neighbours in the grid
 // are on different dies: up to 32 gate rows are dealt to them in turn, so that of 8 each
-// die walks one, with its own address translation (8 gate rows of 2048 rows of 8192 bf16
-// forward 188 us against 215 with neighbours on one gate row, backward 335 and 370; of
-// 4096 97 and 105, 157 and 170; but 64 of 256 rows 100 and 94 forward).
+// die walks one (8 gate rows of 2048 rows of 8192 bf16 forward 185 to 188 us against 215
+// with neighbours on one gate row, backward 335 and 370; of 4096 97 and 105, 157 and 170;
+// but 64 of 256 rows 100 and 94 forward).
 struct BlockPlace {
   int gate_row, slice;
 };
@@ -267,7 +267,7 @@ __device__ __forceinline__ BlockPlace place_of(int slices) {
 // KEEP: the vectors stay in registers; of 16 waves to a row none are left, and LDS
 // holds the factors, the summands (where there are any) are read with each row.
 // Measured: 16384 x 8192 bf16 178 to 187 us (5.8 to 6.0 TB/s), 8192 x 16384 204, 4000 x 5000
-// f16 36 (160 MB), one row of 4096 3.7.
+// f16 33 (160 MB), one row of 4096 3.8.
 template <int DT, int W, int K, bool EACH, bool TINY>
 __global__ __launch_bounds__(NormShape<W>::THREADS) void block_norm_kernel(BlockNormArgs a) {
   using C = RowChunk<DT>;
@@ -470,8 +470,8 @@ __device__ __forceinline__ void keep_saved(V (&v)[K]) {
 // AHEAD: the next row is loaded ahead, KEPT: gamma and post_gamma stay in
 // registers, where the sums leave room for them.
 // Measured (this kernel alone): 16384 x 8192 bf16 from 8-bit rows 250 us (5.1 TB/s, the
-// vector units issuing 54 % of the time), 4001 x 1023 binary32 23.7 (four turns of
-// rows that are not aligned), 128 x 1024 f16 7.2.
+// vector units issuing 54 % of the time), 4001 x 1023 binary32 23.5 (four turns of
+// rows that are not aligned), 128 x 1024 f16 7.4.
 template <int DT, bool BYTES, int W, int K, int WAVES, bool RMS, bool TINY>
 __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArgs a) {
   using C = RowChunk<DT>;
