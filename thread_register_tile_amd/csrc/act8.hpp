@@ -189,11 +189,11 @@ __device__ __forceinline__ void act8_restore(const Act8Args& a, int64_t ldo, int
 #pragma unroll
   for (int j = 0; j < U; ++j) {
     if (row[j] >= a.rows || col[j] >= n) continue;
-    char* p = static_cast<char*>(a.out) + row[j] * ldo * (int64_t)sizeof(typename C::Elem);
+    typename C::Elem* p = static_cast<typename C::Elem*>(a.out) + row[j] * ldo;
     const float s = Q::step(byte[j]);
     if (WHOLE || col[j] + VEC <= n) {
       using Word4 = std::conditional_t<WHOLE, u32x4, typename C::Word4>;
-      *reinterpret_cast<Word4*>(p + col[j] * (int)sizeof(typename C::Elem)) = Q::restore(q[j], s);
+      *reinterpret_cast<Word4*>(p + col[j]) = Q::restore(q[j], s);
     } else {
       float y[VEC];
 #pragma unroll
