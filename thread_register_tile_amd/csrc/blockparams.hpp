@@ -81,9 +81,12 @@ __global__ __launch_bounds__(64 * kBlockParamsWaves) void block_params_kernel(Bl
       s0 = meet(0, s0);
       s1 = meet(1, s1);
     }
-    if (c < a.cols && g < a.groups && (!shared || wave == 0))
-      put_value(a.dgate, a.gdt, g * a.lddg + c,
-                s1 * value_at(a.post_gamma, a.pdt, c, 1.f) + s0 * value_at(a.post_beta, a.pdt, c, 0.f));
+    if (c < a.cols && g < a.groups && (!shared || wave == 0)) {
+      // (without post_beta the sum of e is no part of it, whatever it came to)
+      float v = s1 * value_at(a.post_gamma, a.pdt, c, 1.f);
+      if (a.post_beta) v += s0 * value_at(a.post_beta, a.pdt, c, 0.f);
+      put_value(a.dgate, a.gdt, g * a.lddg + c, v);
+    }
     if (shared) __syncthreads();
   }
 }
