@@ -639,8 +639,10 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
 #pragma unroll
     for (int v = 0; v < K * VEC / 4; ++v) kept[0][v][threadIdx.x] = kept[1][v][threadIdx.x] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  // One row; a wave whose row lies past the end works on zeros, with rstd = 0, and
-  // stores nothing.
+  // One row; a wave whose row lies past the end (in its last turn) works on zeros,
+  // with rstd = 0, and stores nothing.  Gamma and the gate are zero for it too, or one
+  // that is not finite would make NaN of them.
+  static_assert(GROUPS == 1 || KEPT, "a wave without a row clears its gamma");
   auto body = [&](Row& row, Row& next) __attribute__((always_inline)) {
     const bool live = GROUPS == 1 || r < end;
     if constexpr (AHEAD) load_row(next, r + step);
@@ -667,6 +669,11 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
         dh[k] = dr[k] = none;
         x[k] = y[k] = Saved{};
         xstep[k] = ystep[k] = 0.f;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          g1[KEPT ? k : 0][e] = 0.f;
+          asm volatile("" : "+v"(g1[KEPT ? k : 0][e]));   // keeps the branch
+        }
       }
     // addresses and column tests made anew for each pass over a long row: kept
     // they would take a third of the registers
@@ -803,6 +810,9 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArg
         // the gate's own gradient, and the gate into e
         float gate[VEC];
         load_values<DT, TINY>(row_of(a.gate, a.wide_gate, live ? r : 0, a.ldg, E), a.wide_gate, col(k), n, whole(k), 1.f, gate);
+        if (!live)
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) gate[e] = 0.f;
         if (a.dgate && live && col(k) < n) {
           float pg[VEC], pb[VEC];
           load_values<DT, TINY>(a.post ? a.post_gamma : nullptr, a.wide_params, col(k), n, whole(k), 1.f, pg);
