@@ -1150,7 +1150,7 @@ def block_norm_bwd(dh, dr_out, r_out, y, gate=None, *, post=True, post_gamma=Non
     up = dr_out if dh is None else dh
     if up is None:
         raise TrtError(ERR_NULL, "dh or dr_out must be given")
-    rows, cols, ld = _rows(up, "dh")
+    rows, cols, ld = _rows(up, "dr_out" if dh is None else "dh")
     if dr_out is not None and (dr_out.shape != up.shape or dr_out.dtype != up.dtype):
         raise TrtError(ERR_SIZE, f"dr_out must be {list(up.shape)} of {up.dtype}")
     if dh is not None and r_out is None:
