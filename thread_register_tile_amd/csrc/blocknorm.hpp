@@ -49,7 +49,8 @@ __device__ __forceinline__ const char* row_of(const void* p, bool wide, int64_t 
 // 8192 bf16 backward from 8-bit rows 398 us, 266 without).  A row of n >= VEC
 // elements is read VEC at a time from no further than its last VEC, and `fix`
 // shifts out what lies before the chunk (all of it, where the chunk lies past the
-// row): zeros take its place.  Stores go through a descriptor of the row, at an
+// row): zeros take its place.  (The gradient of a gate for every row is stored under
+// a condition all the same, and its gate read in the middle of the row.)  Stores go through a descriptor of the row, at an
 // offset beyond it where the chunk is not whole; the cut chunk of a row whose
 // length VEC does not divide follows in pieces.
 // TINY: rows of fewer than VEC elements, read one by one.
@@ -266,8 +267,8 @@ __device__ __forceinline__ BlockPlace place_of(int slices) {
 // rows lie in one gate row, and gate and post norm's parameters are one product.
 // KEEP: the vectors stay in registers; of 16 waves to a row none are left, and LDS
 // holds the factors, the summands (where there are any) are read with each row.
-// Measured: 16384 x 8192 bf16 178 to 187 us (5.8 to 6.0 TB/s), 8192 x 16384 204, 4000 x 5000
-// f16 33 (160 MB), one row of 4096 3.8.
+// Measured: 16384 x 8192 bf16 178 to 190 us (5.7 to 6.0 TB/s), 8192 x 16384 185 to 204 (8 to 23
+// spilled registers), 4000 x 5000 f16 33 (160 MB), one row of 4096 3.8 to 4.
 template <int DT, int W, int K, bool EACH, bool TINY>
 __global__ __launch_bounds__(NormShape<W>::THREADS) void block_norm_kernel(BlockNormArgs a) {
   using C = RowChunk<DT>;
@@ -465,20 +466,23 @@ __device__ __forceinline__ void keep_saved(V (&v)[K]) {
 // takes that row's rows in turn, GROUPS at a time.  Three rounds of sums: the
 // means of r' and y; the spreads, mean(t), mean(t rhat); mean(s), mean(s yhat).
 // RMS: without the means, two rounds, of three sums and one (16384 x 8192 bf16 from
-// 8-bit rows 250 to 265 us against 310: the arithmetic, 40 instructions an element
+// 8-bit rows 250 to 265 us a call against 310: the arithmetic, 40 instructions an element
 // and a fifth more with the means, takes over half the memory's time).
 // AHEAD: the next row is loaded ahead, KEPT: gamma and post_gamma stay in
 // registers, where the sums leave room for them.
-// Measured (this kernel alone): 16384 x 8192 bf16 from 8-bit rows 250 us (5.1 TB/s, the
-// vector units issuing 54 % of the time), 4001 x 1023 binary32 23.5 (four turns of
-// rows that are not aligned), 128 x 1024 f16 7.4.
+// Measured (this kernel alone): 16384 x 8192 bf16 from 8-bit rows 250 us in a long run of
+// calls (5.5 TB/s of 1386 MB), up to 304 in its tenth to twentieth call, before the part's clock
+// has settled (5.0 TB/s over the first 20; the vector units issue 54 % of the time);
+// 4001 x 1023 binary32 23.9 (four turns of rows that are not aligned), 128 x 1024 f16 7.
 template <int DT, bool BYTES, int W, int K, int WAVES, bool RMS, bool TINY>
 __global__ __launch_bounds__(64 * WAVES) void block_norm_bwd_kernel(BlockNormArgs a) {
   using C = RowChunk<DT>;
   using Q = Act8Chunk<DT>;
   using IO = RowIO<DT, TINY>;
   constexpr int VEC = C::VEC, LANES = 64 * W, GROUPS = WAVES / W, E = sizeof(typename C::Elem);
-  // of 256, 168 and 128 registers; HELD: the rows, e and the sums
+  // of 256, 168 and 128 registers; HELD: the rows, e and the sums.  (Workgroups of 12
+  // and 16 waves spill 1 to 30 registers all the same: an estimate that counted the
+  // addresses and constants would drop the next row or the vectors instead.)
   constexpr int ROOM = WAVES <= 8 ? 216 : WAVES <= 12 ? 118 : 78;
   // of long rows LDS holds what the registers do not: gamma and post_gamma, or of
   // 16 waves of 16-bit rows dgamma's and dbeta's sums

@@ -31,6 +31,7 @@ struct BlockNormArgs {
   void* dgate;           // a gate of its own for every row: written with dr and dy
   int64_t lddg;
   float* part;           // [groups * slices][4][cols] sums of e, e yhat, dh, dh rhat; or null
+                         // (gate rows of few rows have a slice each)
   int32_t slices;        // workgroups to a gate row (both passes)
 };
 
@@ -45,8 +46,9 @@ struct BlockParamsArgs {
   int32_t pdt, gdt;
 };
 
-// Longest row: 32 KiB, of which a workgroup of 8 waves holds four in registers
-// with their sums.
+// Longest row: 32 KiB, two 16-byte chunks for each lane of 16 waves, whose 128
+// registers do not hold more backward (they spill already, with 64 KiB of vectors or
+// 128 KiB of sums in LDS).
 constexpr int64_t kBlockMaxRowBytes = 32768;
 
 // How the backward pass's rows are dealt: `groups` gate rows (one, where the
