@@ -705,9 +705,10 @@ trt_status trt_act8_weight_grad(int64_t tokens, int64_t outputs, int64_t inputs,
  * rms.  h comes of r_out before its rounding; the backward pass takes r_out and
  * y as they are given and forms their norms again.  Sums are binary32 as the
  * layer norm's, each result is rounded once, and results repeat bit for bit.  A
- * row whose squares sum to 2^128 or more has no norm (h: 0 or NaN).  dgate of a
- * gate row of several rows is post_gamma * (sum of e * N(y)) + post_beta * (sum
- * of e): under post_beta two infinite sums may meet as NaN.
+ * row whose squares sum to 2^128 or more has no norm (h: 0 or NaN).  Under a
+ * gate row of several rows the sums are those of e and of e * N(y), which the gate,
+ * post_gamma and post_beta then multiply: one that passes binary32 is infinite
+ * whatever they are, and with post_beta two infinite ones may meet as NaN in dgate.
  *
  * r, y, r_out, h, dh, dr_out, dr, dy: rows x cols of dtype (TRT_F16, TRT_BF16 or
  * TRT_F32), leading dimensions in elements: inputs >= 1, outputs >= cols.  h may be
